@@ -465,6 +465,169 @@ int psa_verify_shared_tree_fwd(const void *q_draft, const void *k_draft, const v
                                int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Around the attention of a layer: the norm and the position rotation of
+ * queries and keys, and the KV cache's rows.
+ * --------------------------------------------------------------------- */
+
+/* What is done to the rows x [d] of queries and keys, in this order:
+ *   norm      x * w / sqrt(mean(x^2) + eps), with q_weight or k_weight [d]
+ *             (NULL: no norm of that kind);
+ *   rotation  pairs (a, b) of the first rot_dim elements become
+ *             (a c - b s, a s + b c); the other elements pass through.
+ * All in fp32, rounded once at the store. */
+typedef struct psa_norm_rope {
+    const int32_t *positions;  /* device [T]: the token's row of cos_sin */
+    const float *cos_sin;      /* device [n_positions, rot_dim] fp32: rot_dim/2 cosines,
+                                  then rot_dim/2 sines; NULL: no rotation */
+    int64_t n_positions;
+    int32_t rot_dim;           /* a multiple of 16, at most d */
+    int32_t interleaved;       /* pair i: elements (2i, 2i+1); 0: (i, i + rot_dim/2) */
+    const void *q_weight;      /* device [d] */
+    const void *k_weight;
+    int32_t weight_dtype;      /* PSA_BF16 or PSA_F32 */
+    float eps;                 /* >= 0, finite */
+} psa_norm_rope;
+
+/*
+ * Norm and rotation of every query and key head in one pass.
+ *   q, k      device [T, Hq, d] / [T, Hkv, d] in dtype; the heads of a token
+ *             are dense, tokens are q_stride / k_stride elements apart (so
+ *             both can be slices of one projection's output).  Strides are
+ *             multiples of 16 bytes.  Either may be NULL (with its output).
+ *   q_out, k_out  device, dense, same dtype (written; may not overlap the
+ *             inputs unless they are the same dense tensor)
+ * d in {64, 128, 256}.  A position outside [0, n_positions) sets
+ * PSA_ERR_INVALID_ARG in dev_status and its token's rows are not written.
+ */
+int psa_qk_norm_rope_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         int dtype, int32_t T, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                         const psa_norm_rope *how, void *q_out, void *k_out,
+                         int32_t *dev_status, void *stream);
+
+/* Workspace of the backward (partial weight gradients), 256-B aligned. */
+size_t psa_qk_norm_rope_bwd_workspace_size(int32_t head_dim);
+
+/*
+ * Its gradients.  With g the upstream gradient turned back by the token's
+ * angle and r = 1 / sqrt(mean(x^2) + eps):
+ *   dx = r (w g - x r^2 mean(w g x)),   dw = sum over all rows of g x r
+ * (without a norm dx = g).  q, k are the forward's inputs (only read where a
+ * norm was applied).
+ *   dq_out, dk_out  device dense [T, Hq, d] / [T, Hkv, d]: upstream gradients
+ *   dq, dk          device, token strides dq_stride / dk_stride elements
+ *                   (written; may be slices of one gradient tensor)
+ *   dq_weight, dk_weight  device [d] fp32 (written, not added to; nullable)
+ * The order of every sum depends on the sizes alone, so results repeat.
+ * A token whose position is outside the table is left out, as above.
+ */
+int psa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *dq_out, const void *dk_out, int dtype, int32_t T,
+                         int32_t Hq, int32_t Hkv, int32_t head_dim, const psa_norm_rope *how,
+                         void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                         float *dq_weight, float *dk_weight, void *workspace, size_t ws_bytes,
+                         int32_t *dev_status, void *stream);
+
+/*
+ * The serving form of the same pass: queries out, and the new tokens' keys
+ * (normed and rotated) and values written to their cache rows.
+ *   q, k, v   device bf16 [T, Hq, d] / [T, Hkv, d] with token strides as
+ *             above; q (with q_out) may be NULL
+ *   how       NULL: rows are written as they are
+ *   k_cache, v_cache  device [n_cache_tokens, Hkv, d]: bf16, or with
+ *             e4m3_scales e4m3 codes of x / scale, saturated at +-448
+ *             (a code stands for scale * e4m3, as in psa_verify_fp8_fwd)
+ *   dev_slots device int32 [T]: token t's cache row; negative: the token is
+ *             padding, nothing of it is cached (its query is still written).
+ *             A row >= n_cache_tokens sets PSA_ERR_INVALID_ARG in dev_status
+ *             and is skipped.  Two tokens with one row race: that row is void.
+ *   q_out     device bf16 dense [T, Hq, d] (written)
+ * d in {64, 128, 256}.  Cache rows that no slot names are left as they were.
+ */
+int psa_cache_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv,
+                     int32_t head_dim, const psa_norm_rope *how, void *k_cache, void *v_cache,
+                     int64_t n_cache_tokens, const int32_t *dev_slots,
+                     const psa_kv_scales *e4m3_scales, void *q_out, int32_t *dev_status,
+                     void *stream);
+
+/*
+ * Cache rows back to dense bf16: k[i] = k_cache[dev_rows[i]] (times k_scale
+ * for an e4m3 cache), v alike.
+ *   dev_rows  device int32 [n] (a slice of a page table); a row outside the
+ *             cache gives zeros and sets PSA_ERR_INVALID_ARG in dev_status
+ *   k, v      device bf16 [n, Hkv, d] (written)
+ * d in {64, 128, 256}.
+ */
+int psa_cache_read(const void *k_cache, const void *v_cache, int64_t n_cache_tokens,
+                   const int32_t *dev_rows, int64_t n, int32_t Hkv, int32_t head_dim,
+                   const psa_kv_scales *e4m3_scales, void *k, void *v, int32_t *dev_status,
+                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * Chunk attention: each request's new tokens over its cached keys.
+ * --------------------------------------------------------------------- */
+
+/* What a chunk plan was built for, and what a call with it needs (host). */
+typedef struct psa_chunk_info {
+    int32_t B, Hq, Hkv, head_dim, window;
+    int32_t n_rows;     /* new tokens of all requests */
+    int32_t n_ctas;     /* CTAs of the launch */
+    int32_t n_units;    /* pieces of work */
+    int32_t n_joins;    /* query blocks whose keys are split over several units */
+    int32_t max_join_rows;  /* query rows of the largest such block */
+    int64_t n_keys;     /* key positions of all requests */
+    int64_t part_rows;  /* rows of partial results */
+    int64_t len;        /* int32 words of the plan */
+} psa_chunk_info;
+
+/* Work plan of psa_chunk_fwd (host only).  Request b has qo_lens[b] new
+ * tokens and kv_lens[b] >= qo_lens[b] keys, the new tokens' own among them.
+ * The query rows of a KV head (tokens x the query heads of its group) are cut
+ * into blocks of 2 * floor(128 / (Hq / Hkv)) tokens, each block's keys into
+ * pieces, and the pieces are handed to n_ctas lists (n_ctas: the CTAs that
+ * run at once, one per SM) so that the longest list is as short as a greedy
+ * longest-first assignment makes it.  window > 0: a token sees its last
+ * `window` keys only (itself included); 0: all.
+ * out: the plan, to be copied to 16-byte aligned device memory; PSA_ERR_CAPACITY (with
+ * info->len set) if cap is smaller.  PSA_ERR_INVALID_ARG for a negative length,
+ * kv_lens[b] < qo_lens[b], or totals beyond 2^31 - 1; PSA_ERR_UNSUPPORTED for a
+ * head_dim other than 64 or 128 or Hq / Hkv above 128. */
+int psa_build_chunk_plan(const int32_t *qo_lens, const int32_t *kv_lens, int32_t B, int32_t Hq,
+                         int32_t Hkv, int32_t head_dim, int32_t window, int32_t n_ctas,
+                         int32_t *out, int64_t cap, psa_chunk_info *info);
+
+/* Bytes of device workspace of a call with this plan, 256-B aligned (at least
+ * 256).  Calls in flight at the same time need a workspace each. */
+size_t psa_chunk_workspace_size(const psa_chunk_info *info);
+
+/*
+ *   q          device [T, Hq, d] bf16, T >= info->n_rows: the new tokens,
+ *              request-major; rows behind n_rows are neither read nor written
+ *   k_cache, v_cache  device [n_cache_tokens, Hkv, d], bf16 or (with
+ *              e4m3_scales) e4m3 standing for k_scale * e4m3, v_scale * e4m3
+ *   dev_kv_indices  NULL: key position t (flat over the requests in order) is
+ *              cache row t; else device int32 [n_keys], its row kv_indices[t];
+ *              a row outside the cache reads as zeros and sets
+ *              PSA_ERR_INVALID_ARG in dev_status
+ *   logit_cap  0: none; c > 0: logits become c tanh(logit / c) before the mask
+ *   o          device [T, Hq, d] bf16 (written up to n_rows)
+ *   lse        device [T, Hq] fp32 (written up to n_rows; nullable)
+ * Token i of request b is at position kv_lens[b] - qo_lens[b] + i and sees the
+ * keys up to its own position, the last `window` of them if the plan has a
+ * window.  The cache must hold the new tokens' keys already
+ * (psa_cache_append).  With an e4m3 cache |q| must stay below 65504 (queries
+ * and probabilities are widened to f16 there).  A value (not a key) that is
+ * not finite spoils every row of its 256-row block that shares its tile, as
+ * in psa_prefill_fwd; rows of other requests and unused cache rows are never
+ * touched.
+ */
+int psa_chunk_fwd(const void *q, const void *k_cache, const void *v_cache,
+                  int64_t n_cache_tokens, const int32_t *dev_kv_indices,
+                  const psa_kv_scales *e4m3_scales, void *o, float *lse, int32_t T, float scale,
+                  float logit_cap, const psa_chunk_info *info, const int32_t *dev_plan,
+                  void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
  * Shared-latent sparse attention                     [MLA] environment,
  * analysis (head-blocked tiles; the latent is shared by every head)
  * --------------------------------------------------------------------- */

@@ -40,7 +40,9 @@ EXPORTS = [
     "psa_verify_shared_tree_fwd",
     "psa_verify_fp8_fwd", "psa_transpose_spec", "psa_prefill_bwd_tiles",
     "psa_prefill_bwd_workspace_size", "psa_prefill_bwd", "psa_verify_tree_fwd",
-    "psa_verify_extend_fwd",
+    "psa_verify_extend_fwd", "psa_qk_norm_rope_fwd", "psa_qk_norm_rope_bwd_workspace_size",
+    "psa_qk_norm_rope_bwd", "psa_cache_append", "psa_cache_read", "psa_build_chunk_plan",
+    "psa_chunk_workspace_size", "psa_chunk_fwd",
 ]
 
 
@@ -69,6 +71,25 @@ class VerifyFeatures(ctypes.Structure):
 class KvScales(ctypes.Structure):
     """psa_kv_scales: per-tensor scales of an e4m3 KV cache."""
     _fields_ = [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class NormRope(ctypes.Structure):
+    """psa_norm_rope: the norm and rotation of query and key rows."""
+    _fields_ = [("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("n_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class ChunkInfo(ctypes.Structure):
+    """psa_chunk_info: what a chunk plan was built for."""
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("n_rows", ctypes.c_int32), ("n_ctas", ctypes.c_int32),
+                ("n_units", ctypes.c_int32), ("n_joins", ctypes.c_int32),
+                ("max_join_rows", ctypes.c_int32), ("n_keys", ctypes.c_int64),
+                ("part_rows", ctypes.c_int64), ("len", ctypes.c_int64)]
 
 
 _lib = None
@@ -152,6 +173,17 @@ def load(path: str):
                                         I32, P, ctypes.c_size_t, P, P], ctypes.c_int),
         "psa_verify_shared_fwd": ([P, P, P, P, P, I64, P, P, I32, I32, I32, I32, I32, F, I32, P,
                                    ctypes.c_size_t, P, P], ctypes.c_int),
+        "psa_qk_norm_rope_fwd": ([P, I64, P, I64, ctypes.c_int, I32, I32, I32, I32, P, P, P, P,
+                                  P], ctypes.c_int),
+        "psa_qk_norm_rope_bwd_workspace_size": ([I32], SZ),
+        "psa_qk_norm_rope_bwd": ([P, I64, P, I64, P, P, ctypes.c_int, I32, I32, I32, I32, P, P,
+                                  I64, P, I64, P, P, P, SZ, P, P], ctypes.c_int),
+        "psa_cache_append": ([P, I64, P, I64, P, I64, I32, I32, I32, I32, P, P, P, I64, P, P, P,
+                              P, P], ctypes.c_int),
+        "psa_cache_read": ([P, P, I64, P, I64, I32, I32, P, P, P, P, P], ctypes.c_int),
+        "psa_build_chunk_plan": ([P, P, I32, I32, I32, I32, I32, I32, P, I64, P], ctypes.c_int),
+        "psa_chunk_workspace_size": ([P], SZ),
+        "psa_chunk_fwd": ([P, P, P, I64, P, P, P, P, I32, F, F, P, P, P, SZ, P, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -526,4 +558,276 @@ def verify_extend(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr: torch.
                                      float(scale), ns, ctypes.byref(feat), _ptr(workspace),
                                      workspace.numel(), _ptr(status), _stream(q_draft.device))
     _check(rc, "psa_verify_extend_fwd")
+    return out, lse
+
+
+# ---------------------------------------------------------------- around a layer's attention
+
+def _launch(name: str, device, *args):
+    """Calls ``name`` on ``device``'s current stream, with ``device`` current
+    (launches and tensor maps belong to the current device's context)."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != PSA_OK:
+        raise PsaError(rc, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, shape, dtype, device, name: str):
+    """A contiguous CUDA tensor of this shape, dtype and device."""
+    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {tuple(shape)} on {device} is "
+                         f"needed, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _rows(t, dtype, device, name: str):
+    """[T, H, d] with dense heads, tokens any distance apart: (T, H, d, token stride)."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: a {dtype} CUDA tensor [T, H, d] is needed on {device}")
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if (H > 1 and sh != d) or sd != 1:
+        raise ValueError(f"{name}: the heads of a token have to be dense")
+    return T, H, d, st if T > 1 else H * d
+
+
+_WEIGHT_DTYPES = {torch.bfloat16: PSA_BF16, torch.float32: PSA_F32}
+
+
+def _norm_rope(T: int, d: int, device, positions, cos_sin, q_weight, k_weight, eps, interleaved):
+    """The psa_norm_rope of these arguments (the tensors are the caller's)."""
+    how = NormRope()
+    if cos_sin is not None:
+        _need(positions is not None, "a rotation (cos_sin) needs positions")
+        _dense(positions, (T,), torch.int32, device, "positions")
+        _need(cos_sin.dim() == 2, "cos_sin: [positions, rot_dim] is needed")
+        _dense(cos_sin, cos_sin.shape, torch.float32, device, "cos_sin")
+        how.positions, how.cos_sin = positions.data_ptr(), cos_sin.data_ptr()
+        how.n_positions, how.rot_dim = cos_sin.shape
+        how.interleaved = int(interleaved)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        _need(w.dtype in _WEIGHT_DTYPES, f"{name}: bf16 or fp32 weights are needed")
+        _dense(w, (d,), w.dtype, device, name)
+        setattr(how, name, w.data_ptr())
+        how.weight_dtype = _WEIGHT_DTYPES[w.dtype]
+    _need(q_weight is None or k_weight is None or q_weight.dtype == k_weight.dtype,
+          "q_weight and k_weight have to be of one dtype")
+    how.eps = float(eps)
+    return how
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, status=None):
+    """RMS norm of every query and key head (where a weight [d] is given) and
+    the position rotation, in one pass: dense (q_out, k_out).
+
+    q [T, Hq, d] and k [T, Hkv, d], bf16 or fp32, may be slices of one
+    projection's output (dense heads, any token stride of whole 16 bytes).
+    positions: device int32 [T]; cos_sin: device fp32 [n_positions, rot_dim],
+    rot_dim/2 cosines then rot_dim/2 sines of every position (None: no
+    rotation).  Pairs are (i, i + rot_dim/2), or (2i, 2i + 1) with
+    ``interleaved``; elements behind rot_dim pass through."""
+    _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
+    dev = q.device
+    T, Hq, d, qs = _rows(q, q.dtype, dev, "q")
+    Tk, Hkv, dk, ks = _rows(k, q.dtype, dev, "k")
+    _need(Tk == T and dk == d, "q and k have to agree in tokens and head size")
+    how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
+    q_out = (torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if q_out is None
+             else _dense(q_out, (T, Hq, d), q.dtype, dev, "q_out"))
+    k_out = (torch.empty((T, Hkv, d), dtype=q.dtype, device=dev) if k_out is None
+             else _dense(k_out, (T, Hkv, d), q.dtype, dev, "k_out"))
+    _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks,
+            _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, ctypes.byref(how), q_out.data_ptr(),
+            k_out.data_ptr(), _addr(status))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None,
+                     workspace=None, status=None):
+    """Gradients of :func:`qk_norm_rope` for the upstream gradients dq_out and
+    dk_out of its outputs: (dq, dk, dq_weight, dk_weight), the weights' in fp32
+    and None where there is no weight.  dq and dk may be given as slices of
+    one gradient tensor (dense heads, any token stride of whole 16 bytes)."""
+    _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
+    dev = q.device
+    T, Hq, d, qs = _rows(q, q.dtype, dev, "q")
+    Tk, Hkv, hd, ks = _rows(k, q.dtype, dev, "k")
+    _need(Tk == T and hd == d, "q and k have to agree in tokens and head size")
+    _dense(dq_out, (T, Hq, d), q.dtype, dev, "dq_out")
+    _dense(dk_out, (T, Hkv, d), q.dtype, dev, "dk_out")
+    how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
+    dq = torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty((T, Hkv, d), dtype=q.dtype, device=dev) if dk is None else dk
+    _need(tuple(dq.shape) == (T, Hq, d) and tuple(dk.shape) == (T, Hkv, d),
+          "dq and dk have to be shaped as q and k")
+    dqs, dks = _rows(dq, q.dtype, dev, "dq")[3], _rows(dk, q.dtype, dev, "dk")[3]
+    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8,
+                                device=dev)
+    _launch("psa_qk_norm_rope_bwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, dq_out.data_ptr(),
+            dk_out.data_ptr(), _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, ctypes.byref(how),
+            dq.data_ptr(), dqs, dk.data_ptr(), dks, _addr(dqw), _addr(dkw), workspace.data_ptr(),
+            workspace.numel(), _addr(status))
+    return dq, dk, dqw, dkw
+
+
+_E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _caches(k_cache, v_cache, k_scale, v_scale, device):
+    """(tokens, heads, d, scales or None) of a pair of cache tensors."""
+    e4m3 = k_scale is not None or v_scale is not None
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(c.dim() == 3 and c.is_contiguous() and c.device == device and c.is_cuda,
+              f"{name}: a contiguous tensor [tokens, Hkv, d] on {device} is needed")
+        _need(c.dtype in _E4M3_DTYPES if e4m3 else c.dtype == torch.bfloat16,
+              f"{name}: bf16, or e4m3 bytes with k_scale and v_scale, is needed")
+    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache have to be shaped alike")
+    _need(not e4m3 or (k_scale is not None and v_scale is not None),
+          "an e4m3 cache needs both k_scale and v_scale")
+    sc = ctypes.byref(KvScales(float(k_scale), float(v_scale))) if e4m3 else None
+    return (*k_cache.shape, sc)
+
+
+def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 k_scale: float | None = None, v_scale: float | None = None, q_out=None,
+                 status=None):
+    """The serving form of :func:`qk_norm_rope`: returns the queries (dense
+    bf16 [T, Hq, d]; None for q = None) and writes the tokens' keys, normed and
+    rotated, and values to the cache rows ``slots`` (device int32 [T]; a
+    negative slot is padding: nothing of that token is cached).  With k_scale /
+    v_scale the caches hold e4m3 codes of x / scale, saturated at +-448.
+    Two tokens may not share a row."""
+    dev = k_cache.device
+    ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
+    T, Hk, dk, ks = _rows(k, torch.bfloat16, dev, "k")
+    Tv, Hv, dv, vs = _rows(v, torch.bfloat16, dev, "v")
+    _need((Hk, dk) == (Hkv, d) and (Tv, Hv, dv) == (T, Hkv, d),
+          "k and v have to agree with the caches in heads and head size")
+    Hq, qs = 0, 0
+    if q is not None:
+        Tq, Hq, dq, qs = _rows(q, torch.bfloat16, dev, "q")
+        _need(Tq == T and dq == d, "q, k and v have to agree in tokens and head size")
+        q_out = (torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if q_out is None
+                 else _dense(q_out, (T, Hq, d), torch.bfloat16, dev, "q_out"))
+    _dense(slots, (T,), torch.int32, dev, "slots")
+    how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
+    _launch("psa_cache_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv,
+            d, ctypes.byref(how), k_cache.data_ptr(), v_cache.data_ptr(), ntok, slots.data_ptr(),
+            sc, _addr(q_out) if q is not None else None, _addr(status))
+    return q_out if q is not None else None
+
+
+def cache_read(k_cache, v_cache, rows, k_scale: float | None = None,
+               v_scale: float | None = None, k=None, v=None, status=None):
+    """Cache rows ``rows`` (device int32 [n], e.g. a slice of a page table)
+    as dense bf16 (k, v) [n, Hkv, d]; e4m3 caches are scaled back."""
+    dev = k_cache.device
+    ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
+    n = rows.numel()
+    _dense(rows, (n,), torch.int32, dev, "rows")
+    k = (torch.empty((n, Hkv, d), dtype=torch.bfloat16, device=dev) if k is None
+         else _dense(k, (n, Hkv, d), torch.bfloat16, dev, "k"))
+    v = (torch.empty((n, Hkv, d), dtype=torch.bfloat16, device=dev) if v is None
+         else _dense(v, (n, Hkv, d), torch.bfloat16, dev, "v"))
+    _launch("psa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), ntok, rows.data_ptr(),
+            n, Hkv, d, sc, k.data_ptr(), v.data_ptr(), _addr(status))
+    return k, v
+
+
+class ChunkPlan:
+    """The work plan of :func:`chunk` for given lengths: the device copy of the
+    lists, and what a call needs to know of them (``info``,
+    ``workspace_bytes``).  One plan serves any number of calls."""
+
+    def __init__(self, info: ChunkInfo, data: torch.Tensor, workspace_bytes: int):
+        self.info, self.data, self.workspace_bytes = info, data, workspace_bytes
+
+
+def build_chunk_plan(qo_lens, kv_lens, Hq: int, Hkv: int, head_dim: int, window: int = 0,
+                     n_ctas: int = 148):
+    """(plan as a host int32 array, ChunkInfo) for ``n_ctas`` work lists."""
+    ql = np.ascontiguousarray(np.asarray(qo_lens, dtype=np.int32))
+    kl = np.ascontiguousarray(np.asarray(kv_lens, dtype=np.int32))
+    _need(ql.ndim == 1 and ql.shape == kl.shape, "one query and one key length per request")
+    info = ChunkInfo()
+    out = np.zeros(4096, dtype=np.int32)
+    while True:
+        rc = lib().psa_build_chunk_plan(_ptr(ql), _ptr(kl), len(ql), Hq, Hkv, head_dim,
+                                        int(window), n_ctas, _ptr(out), len(out),
+                                        ctypes.byref(info))
+        if rc == PSA_ERR_CAPACITY and info.len > len(out):
+            out = np.zeros(info.len, dtype=np.int32)
+            continue
+        _check(rc, "psa_build_chunk_plan")
+        return out[:info.len], info
+
+
+def plan_chunk(qo_lens, kv_lens, Hq: int, Hkv: int, head_dim: int, window: int = 0,
+               device="cuda") -> ChunkPlan:
+    """Work plan for :func:`chunk`: request b has qo_lens[b] new tokens and
+    kv_lens[b] cached keys, the new tokens' own included (host lists).
+    window > 0: a token sees its last ``window`` keys only, itself included."""
+    device = torch.device(device)
+    sms = torch.cuda.get_device_properties(device).multi_processor_count
+    data, info = build_chunk_plan(qo_lens, kv_lens, Hq, Hkv, head_dim, window, sms)
+    return ChunkPlan(info, torch.from_numpy(data).to(device),
+                     int(lib().psa_chunk_workspace_size(ctypes.byref(info))))
+
+
+def chunk(q, k_cache, v_cache, plan: ChunkPlan, scale: float, kv_indices=None,
+          logit_cap: float = 0.0, k_scale: float | None = None, v_scale: float | None = None,
+          out=None, lse=None, workspace=None, status=None):
+    """Attention of each request's new tokens over its cached keys: O [T, Hq, d]
+    bf16 and LSE [T, Hq] fp32.
+
+    q [T, Hq, d] bf16 holds the plan's new tokens request by request (rows
+    behind them are left alone); the caches [tokens, Hkv, d], bf16 or (with
+    k_scale / v_scale) e4m3, hold the new tokens' keys already
+    (:func:`cache_append`).  kv_indices: device int32 page table, key position
+    t (flat over the requests) is cache row kv_indices[t]; without it the
+    positions are the cache's first rows.  logit_cap c > 0: logits become
+    c tanh(logit / c)."""
+    dev = q.device
+    info = plan.info
+    ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
+    T = q.shape[0]
+    _dense(q, (T, info.Hq, info.head_dim), torch.bfloat16, dev, "q")
+    _need((Hkv, d) == (info.Hkv, info.head_dim), "the caches do not fit the plan's heads")
+    _need(plan.data.device == dev, "the plan is on another device")
+    if kv_indices is not None:
+        _need(kv_indices.dim() == 1 and kv_indices.numel() >= info.n_keys,
+              f"kv_indices: {info.n_keys} entries are needed")
+        _dense(kv_indices, kv_indices.shape, torch.int32, dev, "kv_indices")
+    out = (torch.empty_like(q) if out is None
+           else _dense(out, q.shape, torch.bfloat16, dev, "out"))
+    lse = (torch.empty((T, info.Hq), dtype=torch.float32, device=dev) if lse is None
+           else _dense(lse, (T, info.Hq), torch.float32, dev, "lse"))
+    if workspace is None:
+        workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
+    _launch("psa_chunk_fwd", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ntok,
+            _addr(kv_indices), sc, out.data_ptr(), lse.data_ptr(), T, float(scale),
+            float(logit_cap), ctypes.byref(info), plan.data.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _addr(status))
     return out, lse

@@ -502,6 +502,234 @@ extern "C" int psa_prefill_fwd(const void* q, const void* k, const void* v, void
   return launch_prefill(a);
 }
 
+// ------------------------------------------------------------------ norm, rotation, cache rows
+
+namespace {
+
+bool ok_scales(const psa_kv_scales* sc) {
+  return !sc || (sc->k_scale > 0.f && sc->v_scale > 0.f && std::isfinite(sc->k_scale) &&
+                 std::isfinite(sc->v_scale));
+}
+
+// A token stride: the token's heads do not overlap the next token's, and
+// every row starts on a 16-byte boundary.
+bool ok_stride(int64_t stride, int32_t H, int32_t d, int elem) {
+  return stride >= int64_t(H) * d && (stride * elem) % 16 == 0;
+}
+
+bool ok_how(const psa_norm_rope* how, int32_t d) {
+  if (how->cos_sin) {
+    if (!how->positions || how->n_positions < 0 || how->rot_dim <= 0 || how->rot_dim > d ||
+        how->rot_dim % 16 != 0 || !aligned16(how->cos_sin) ||
+        (reinterpret_cast<uintptr_t>(how->positions) & 3u))
+      return false;
+  }
+  if (how->q_weight || how->k_weight) {
+    if (how->weight_dtype != PSA_BF16 && how->weight_dtype != PSA_F32) return false;
+    if (!(how->eps >= 0.f) || !std::isfinite(how->eps)) return false;
+    if ((how->q_weight && !aligned16(how->q_weight)) ||
+        (how->k_weight && !aligned16(how->k_weight)))
+      return false;
+  }
+  return true;
+}
+
+bool ok_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+}  // namespace
+
+extern "C" int psa_qk_norm_rope_fwd(const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, int dtype, int32_t T, int32_t Hq,
+                                    int32_t Hkv, int32_t head_dim, const psa_norm_rope* how,
+                                    void* q_out, void* k_out, int32_t* dev_status,
+                                    void* stream) {
+  if ((dtype != PSA_BF16 && dtype != PSA_F32) || T < 0 || !how ||
+      (T > 0 && !q && !k) || (q && Hq <= 0) || (k && Hkv <= 0))
+    return PSA_ERR_INVALID_ARG;
+  if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
+  if (!ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  if (T == 0) return PSA_OK;
+  const int elem = dtype == PSA_F32 ? 4 : 2;
+  if ((q && (!q_out || !aligned16(q) || !aligned16(q_out) ||
+             !ok_stride(q_stride, Hq, head_dim, elem))) ||
+      (k && (!k_out || !aligned16(k) || !aligned16(k_out) ||
+             !ok_stride(k_stride, Hkv, head_dim, elem))))
+    return PSA_ERR_INVALID_ARG;
+  RowsArgs a = {};
+  a.q = q, a.k = k;
+  a.q_stride = q_stride, a.k_stride = k_stride;
+  a.f32 = dtype == PSA_F32;
+  a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = head_dim;
+  a.how = *how;
+  a.q_out = q_out, a.k_out = k_out;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_rows(a);
+}
+
+extern "C" size_t psa_qk_norm_rope_bwd_workspace_size(int32_t head_dim) {
+  return head_dim > 0 ? size_t(kRowsBwdMaxBlocks) * 2 * head_dim * sizeof(float) : 0;
+}
+
+extern "C" int psa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* dq_out, const void* dk_out,
+                                    int dtype, int32_t T, int32_t Hq, int32_t Hkv,
+                                    int32_t head_dim, const psa_norm_rope* how, void* dq,
+                                    int64_t dq_stride, void* dk, int64_t dk_stride,
+                                    float* dq_weight, float* dk_weight, void* workspace,
+                                    size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if ((dtype != PSA_BF16 && dtype != PSA_F32) || T < 0 || !how ||
+      (T > 0 && !q && !k) || (q && Hq <= 0) || (k && Hkv <= 0))
+    return PSA_ERR_INVALID_ARG;
+  if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
+  if (!ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  // a weight gradient needs the norm it belongs to
+  if ((dq_weight && !how->q_weight) || (dk_weight && !how->k_weight) ||
+      (T > 0 && ((dq_weight && !q) || (dk_weight && !k))) ||
+      (reinterpret_cast<uintptr_t>(dq_weight) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dk_weight) & 3u))
+    return PSA_ERR_INVALID_ARG;
+  const int elem = dtype == PSA_F32 ? 4 : 2;
+  if (T > 0 && ((q && (!dq_out || !dq || !aligned16(q) || !aligned16(dq_out) || !aligned16(dq) ||
+                       !ok_stride(q_stride, Hq, head_dim, elem) ||
+                       !ok_stride(dq_stride, Hq, head_dim, elem))) ||
+                (k && (!dk_out || !dk || !aligned16(k) || !aligned16(dk_out) || !aligned16(dk) ||
+                       !ok_stride(k_stride, Hkv, head_dim, elem) ||
+                       !ok_stride(dk_stride, Hkv, head_dim, elem)))))
+    return PSA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < psa_qk_norm_rope_bwd_workspace_size(head_dim) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PSA_ERR_WORKSPACE;
+  RowsBwdArgs b = {};
+  b.rows.q = q, b.rows.k = k;
+  b.rows.q_stride = q_stride, b.rows.k_stride = k_stride;
+  b.rows.f32 = dtype == PSA_F32;
+  b.rows.T = T, b.rows.Hq = Hq, b.rows.Hkv = Hkv, b.rows.D = head_dim;
+  b.rows.how = *how;
+  b.rows.q_out = dq, b.rows.k_out = dk;
+  b.rows.status = dev_status;
+  b.rows.stream = static_cast<cudaStream_t>(stream);
+  b.dq_stride = dq_stride, b.dk_stride = dk_stride;
+  b.dq_out = dq_out, b.dk_out = dk_out;
+  b.part = static_cast<float*>(workspace);
+  b.dq_weight = dq_weight, b.dk_weight = dk_weight;
+  return launch_rows_bwd(b);
+}
+
+extern "C" int psa_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, int32_t T, int32_t Hq,
+                                int32_t Hkv, int32_t head_dim, const psa_norm_rope* how,
+                                void* k_cache, void* v_cache, int64_t n_cache_tokens,
+                                const int32_t* dev_slots, const psa_kv_scales* e4m3_scales,
+                                void* q_out, int32_t* dev_status, void* stream) {
+  if (T < 0 || Hkv <= 0 || (q && Hq <= 0) || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
+      !ok_scales(e4m3_scales))
+    return PSA_ERR_INVALID_ARG;
+  if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
+  if (how && !ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  if (T == 0) return PSA_OK;
+  if (!k || !v || !k_cache || !v_cache || !dev_slots || !aligned16(k) || !aligned16(v) ||
+      !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(dev_slots) & 3u) || !ok_stride(k_stride, Hkv, head_dim, 2) ||
+      !ok_stride(v_stride, Hkv, head_dim, 2) ||
+      (q && (!q_out || !aligned16(q) || !aligned16(q_out) ||
+             !ok_stride(q_stride, Hq, head_dim, 2))))
+    return PSA_ERR_INVALID_ARG;
+  RowsArgs a = {};
+  a.q = q, a.k = k, a.v = v;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = head_dim;
+  if (how) a.how = *how;
+  a.q_out = q_out, a.k_out = k_cache, a.v_out = v_cache;
+  a.slots = dev_slots;
+  a.n_cache = n_cache_tokens;
+  a.e4m3 = e4m3_scales != nullptr;
+  a.k_scale = e4m3_scales ? e4m3_scales->k_scale : 1.f;
+  a.v_scale = e4m3_scales ? e4m3_scales->v_scale : 1.f;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_rows(a);
+}
+
+extern "C" int psa_cache_read(const void* k_cache, const void* v_cache, int64_t n_cache_tokens,
+                              const int32_t* dev_rows, int64_t n, int32_t Hkv, int32_t head_dim,
+                              const psa_kv_scales* e4m3_scales, void* k, void* v,
+                              int32_t* dev_status, void* stream) {
+  if (n < 0 || Hkv <= 0 || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
+      Hkv > INT32_MAX / 256 || !ok_scales(e4m3_scales))
+    return PSA_ERR_INVALID_ARG;
+  if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
+  if (n == 0) return PSA_OK;
+  if (!k_cache || !v_cache || !dev_rows || !k || !v || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(k) || !aligned16(v) ||
+      (reinterpret_cast<uintptr_t>(dev_rows) & 3u))
+    return PSA_ERR_INVALID_ARG;
+  CacheReadArgs a = {};
+  a.kc = k_cache, a.vc = v_cache;
+  a.n_cache = n_cache_tokens;
+  a.rows = dev_rows;
+  a.n = n;
+  a.Hkv = Hkv, a.D = head_dim;
+  a.e4m3 = e4m3_scales != nullptr;
+  a.k_scale = e4m3_scales ? e4m3_scales->k_scale : 1.f;
+  a.v_scale = e4m3_scales ? e4m3_scales->v_scale : 1.f;
+  a.k = k, a.v = v;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_cache_read(a);
+}
+
+// ------------------------------------------------------------------ chunk
+
+extern "C" size_t psa_chunk_workspace_size(const psa_chunk_info* info) {
+  if (!info || info->part_rows <= 0) return 256;
+  const size_t o_bytes = size_t(info->part_rows) * info->head_dim * sizeof(float);
+  const size_t l_bytes = size_t(info->part_rows) * sizeof(float);
+  return (o_bytes + 255) / 256 * 256 + (l_bytes + 255) / 256 * 256;
+}
+
+extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_cache,
+                             int64_t n_cache_tokens, const int32_t* dev_kv_indices,
+                             const psa_kv_scales* e4m3_scales, void* o, float* lse, int32_t T,
+                             float scale, float logit_cap, const psa_chunk_info* info,
+                             const int32_t* dev_plan, void* workspace, size_t ws_bytes,
+                             int32_t* dev_status, void* stream) {
+  if (!info || T < info->n_rows || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
+      !(scale > 0.f) || !std::isfinite(scale) || !(logit_cap >= 0.f) ||
+      !std::isfinite(logit_cap) || !ok_scales(e4m3_scales))
+    return PSA_ERR_INVALID_ARG;
+  if (info->n_rows == 0) return PSA_OK;
+  // without a page table the key positions are the cache's first rows
+  if (!dev_kv_indices && info->n_keys > n_cache_tokens) return PSA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !o || !dev_plan || !aligned16(q) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(o) || !aligned16(dev_plan) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dev_kv_indices) & 3u))
+    return PSA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < psa_chunk_workspace_size(info) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PSA_ERR_WORKSPACE;
+  ChunkArgs a = {};
+  a.q = q, a.kc = k_cache, a.vc = v_cache;
+  a.n_cache = n_cache_tokens;
+  a.kv_indices = dev_kv_indices;
+  a.e4m3 = e4m3_scales != nullptr;
+  a.k_scale = e4m3_scales ? e4m3_scales->k_scale : 1.f;
+  a.v_scale = e4m3_scales ? e4m3_scales->v_scale : 1.f;
+  a.o = o, a.lse = lse;
+  a.T = T;
+  a.scale = scale, a.cap = logit_cap;
+  a.info = *info;
+  a.plan = dev_plan;
+  const size_t o_bytes =
+      (size_t(info->part_rows) * info->head_dim * sizeof(float) + 255) / 256 * 256;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_chunk(a);
+}
+
 // ------------------------------------------------------------------ sparse latent
 
 extern "C" int psa_sparse_latent_fwd(const void* q, const void* latent, const int32_t* idx,

@@ -1,0 +1,901 @@
+// Chunk attention: each request's new tokens over its cached keys (the new
+// tokens' own among them), read through a token-granular page table or from
+// a contiguous range, bf16 or e4m3, optionally within a sliding window and
+// with logits capped by a tanh:
+//   s_ij = scale q_i.k_j           (capped: c tanh(s_ij / c))
+//   p_ij = exp(s_ij) for the keys j in (pos_i - window, pos_i], else 0
+//   o_i  = sum_j p_ij v_j / sum_j p_ij,   lse_i = log sum_j p_ij
+//
+// The work is 4 d FLOP per visible (query row, key) pair, and the cache is
+// read once per block of query rows, so long chunks are bound by the tensor
+// cores and the exponentials, and single tokens by the cache's bytes.
+//
+// A KV head's query rows are packed (token, head of the group) into 128-row
+// tiles, so one K/V tile serves all heads of the group.  A CTA (one per SM)
+// walks its list of units (query block, KV head, key range) with two row
+// halves on one K/V tile stream, or, where the rows fit one half ("twin"),
+// with both halves on the same rows and alternate tiles: then each half keeps
+// its own running max and sum and writes its own partial.
+//   warps 0, 2, 3  loaders.  A page table scatters a tile's keys, so K and V
+//                  rows are gathered with 16-byte asynchronous copies straight
+//                  into the 128-byte-swizzled tiles the MMA reads (zero fill
+//                  behind the key range, so no unused cache row is touched).
+//                  e4m3 rows go through a thread-private staging area and are
+//                  widened to f16 (exact) by the thread that copied them.
+//                  Warp 0 also loads the query rows by TMA.
+//   warp 1         tcgen05 issuer: per half S = Q K^T into TMEM, O += P V with
+//                  P read from TMEM over the S columns.
+//   warps 4..11    softmax of the two halves, one row per thread, running max
+//                  in the log2 domain with lazy rescaling, and the epilogue:
+//                  final rows, or a partial (O / l and log2-sum-exp, fp32) for
+//                  the join kernel.
+// P is rounded to bf16 (f16 over an e4m3 cache) for the tensor cores: at most
+// half a step per weight, averaged over the keys; the sum l keeps fp32.
+// Every wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "psa_chunk.h"
+#include "psa_debug.cuh"
+#include "psa_device.cuh"
+#include "psa_internal.h"
+#include "psa_tmem_wide.cuh"
+
+namespace psa {
+namespace {
+
+constexpr int BM = 128;            // query rows per half
+constexpr int BN = kChunkTile;     // keys per tile
+constexpr int kThreads = 384;      // 12 warps
+constexpr int kLoaders = 3;        // warps 0, 2, 3
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
+// Registers: 384 threads x 168 at launch = 64512 = 128 x 104 (loaders, MMA)
+// + 256 x 200 (softmax: a whole 128-column S row in registers).  The launcher
+// checks the compiled count before the first launch.
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsLow = 104, kRegsSoftmax = 200;
+static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int NPART = D / 64;  // 128-byte swizzle atoms across d
+  static constexpr uint32_t Q_BYTES = BM * D * 2;  // one half
+  static constexpr uint32_t KV_BYTES = BN * D * 2;
+  static constexpr int ROWB = E4M3 ? D : 2 * D;    // bytes of a cached row
+  static constexpr int CPR = ROWB / 16;            // 16-byte copies of a row
+  static constexpr int RPI = 32 / CPR;             // rows per warp instruction
+  static constexpr int NI = BN / RPI;              // warp instructions per tile
+  static constexpr int NPL = (NI + kLoaders - 1) / kLoaders;  // ... of one loader
+  static constexpr uint32_t STAGE_BYTES = E4M3 ? BN * D : 0;  // raw K (or V) tile
+  static constexpr int NSK = D == 64 ? 4 : (E4M3 ? 2 : 3);
+  static constexpr int NSV = D == 64 ? 4 : 2;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + NSK * KV_BYTES;
+  static constexpr uint32_t OFF_STAGE = OFF_V + NSV * KV_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_STAGE + 2 * STAGE_BYTES;
+  static constexpr uint32_t NBAR = 3 + 2 * NSK + 2 * NSV + 8;
+  static constexpr uint32_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
+};
+
+struct Params {
+  const int32_t* plan;
+  int32_t n_ctas, n_units, n_joins;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t n_cache;
+  const int32_t* kv_indices;
+  int64_t n_keys;
+  __nv_bfloat16* o;
+  float* lse;
+  int32_t n_rows, Hq, Hkv, G, TPH, window;
+  float scale_log2;  // logits in the log2 domain; capped: 2 log2e scale / cap
+  float cap_log2;    // cap * log2e
+  float v_scale;
+  float* part_o;
+  float* part_lse;
+  int64_t part_rows;
+  int32_t* status;
+};
+
+// One unit of the plan as every role sees it.
+struct Unit {
+  int q0, ntok, pos0, kvh, kv0, t0, t1, twin, part;
+  bool ok;  // inside the buffers (debug build); otherwise every role skips it
+};
+
+__device__ __forceinline__ Unit load_unit(const Params& p, const int4* units, int u) {
+  const int4 a = __ldg(units + 3 * u), b = __ldg(units + 3 * u + 1);
+  Unit x;
+  x.q0 = a.x, x.ntok = a.y, x.pos0 = a.z, x.kvh = a.w;
+  x.kv0 = b.x, x.t0 = b.y, x.t1 = b.z, x.twin = b.w;
+  x.part = __ldg(reinterpret_cast<const int32_t*>(units + 3 * u + 2));
+  x.ok = psa_in_bounds(
+      x.q0 >= 0 && x.ntok > 0 && x.ntok <= (x.twin ? 1 : 2) * p.TPH &&
+          int64_t(x.q0) + x.ntok <= p.n_rows && x.kvh >= 0 && x.kvh < p.Hkv && x.kv0 >= 0 &&
+          x.t0 >= 0 && x.t1 > x.t0 && int64_t(x.kv0) + x.t1 <= p.n_keys && x.part >= -1 &&
+          int64_t(x.part) + (x.twin ? 2 : 1) * x.ntok * p.G <= p.part_rows + (x.part < 0),
+      p.status);
+  return x;
+}
+
+// Tokens and first position of half x (both halves have the same in a twin).
+__device__ __forceinline__ int half_tokens(const Unit& u, int x, int TPH) {
+  return u.twin ? u.ntok : (x ? u.ntok - TPH : min(u.ntok, TPH));
+}
+__device__ __forceinline__ int half_pos(const Unit& u, int x, int TPH) {
+  return u.pos0 + (u.twin ? 0 : x * TPH);
+}
+
+// Whether half x takes part in the tile at key t.
+__device__ __forceinline__ bool half_sees(const Unit& u, int x, int t, int TPH, int window) {
+  if (u.twin) return (((t - u.t0) >> 7) & 1) == x;
+  const int first = half_pos(u, x, TPH), n = half_tokens(u, x, TPH);
+  return t <= first + n - 1 && (window == 0 || min(t + BN, u.t1) - 1 > first - window);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
+// Arrives on `bar` once every cp.async this thread issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait1() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+
+// Four e4m3 codes to two f16 pairs (exact).
+__device__ __forceinline__ uint2 e4m3x4_to_f16(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16(lo, hi);
+  }
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bits [a, b) of a 128-bit mask.
+__device__ __forceinline__ void range_bits(uint32_t (&m)[4], int a, int b) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int lo = min(max(a - 32 * w, 0), 32), hi = min(max(b - 32 * w, 0), 32);
+    const uint32_t below_hi = hi == 32 ? 0xffffffffu : ((1u << hi) - 1u);
+    const uint32_t below_lo = lo == 32 ? 0xffffffffu : ((1u << lo) - 1u);
+    m[w] = below_hi & ~below_lo;
+  }
+}
+
+// kind::f16 with f16 or bf16 operands and fp32 accumulation.
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc_of(uint32_t M, uint32_t N, bool b_mn) {
+  return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(b_mn) << 16) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <int D, bool E4M3, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, Params p) {
+  using C = Cfg<D, E4M3>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ChunkPlanView view(p.n_ctas, p.n_units, p.n_joins);
+  if (__ldg(p.plan) != kChunkMagic || __ldg(p.plan + 1) != p.n_ctas ||
+      __ldg(p.plan + 2) != p.n_units || __ldg(p.plan + 3) != p.n_joins) {
+    if (threadIdx.x == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
+    return;
+  }
+  const int4* units = reinterpret_cast<const int4*>(p.plan + view.units);
+  int u_first = __ldg(p.plan + view.lists + blockIdx.x);
+  int u_end = __ldg(p.plan + view.lists + blockIdx.x + 1);
+  if (!psa_in_bounds(u_first >= 0 && u_first <= u_end && u_end <= p.n_units, p.status))
+    u_first = u_end = 0;
+
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bar;       // TMA bytes
+  uint64_t* q_conv = bar + 1;   // e4m3: the softmax warps have widened Q to f16
+  uint64_t* q_empty = bar + 2;  // MMA commit
+  uint64_t* k_full = bar + 3;
+  uint64_t* k_empty = k_full + C::NSK;
+  uint64_t* v_full = k_empty + C::NSK;
+  uint64_t* v_empty = v_full + C::NSV;
+  uint64_t* s_full = v_empty + C::NSV;  // [2] each, one per half
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_free = pv_done + 2;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(q_full, 1);
+    mbar_init(q_conv, 8);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::NSK; ++i) {
+      mbar_init(k_full + i, kLoaders * 32);
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < C::NSV; ++i) {
+      mbar_init(v_full + i, kLoaders * 32);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full + x, 1);
+      mbar_init(p_full + x, 4);
+      mbar_init(pv_done + x, 1);
+      mbar_init(o_free + x, 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
+    if (warp != 1) {
+      // ================================================================ loaders
+      const int li = warp == 0 ? 0 : warp - 1;
+      const int sub = lane / C::CPR, chunk = lane % C::CPR;
+      if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_q);
+      int u = u_first;
+      Unit cur = {}, nxt = {};
+      auto next_unit = [&](int from) {
+        for (u = from; u < u_end; ++u) {
+          nxt = load_unit(p, units, u);
+          if (nxt.ok) return true;
+        }
+        return false;
+      };
+      // cache rows of this lane's copies of the tile at key t (-1: zeros)
+      auto lookup = [&](const Unit& x, int t, int32_t (&e)[C::NPL]) {
+#pragma unroll
+        for (int n = 0; n < C::NPL; ++n) {
+          const int i = li + kLoaders * n;
+          const int pos = t + i * C::RPI + sub;
+          e[n] = -1;
+          if (i < C::NI && pos < x.t1) {
+            const int64_t flat = int64_t(x.kv0) + pos;
+            e[n] = p.kv_indices ? __ldg(p.kv_indices + flat) : int32_t(flat);
+          }
+        }
+      };
+      auto check = [&](const Unit& x, int t, int32_t (&e)[C::NPL]) {
+#pragma unroll
+        for (int n = 0; n < C::NPL; ++n) {
+          const int i = li + kLoaders * n;
+          const bool live = i < C::NI && t + i * C::RPI + sub < x.t1;
+          if (live && (e[n] < 0 || e[n] >= p.n_cache)) {
+            report_status(p.status, PSA_ERR_INVALID_ARG);
+            e[n] = -1;
+          }
+        }
+      };
+      const size_t row_bytes = size_t(p.Hkv) * C::ROWB;
+      // one tile of K or V: asynchronous copies of this lane's pieces, into
+      // the tile (bf16) or the staging area (e4m3)
+      auto copy_rows = [&](const uint8_t* cache, const int32_t (&e)[C::NPL], uint32_t dst) {
+#pragma unroll
+        for (int n = 0; n < C::NPL; ++n) {
+          const int i = li + kLoaders * n;
+          if (i < C::NI) {
+            const int row = i * C::RPI + sub;
+            const bool live = e[n] >= 0;
+            const uint8_t* src = cache + size_t(live ? e[n] : 0) * row_bytes;
+            const uint32_t at =
+                E4M3 ? uint32_t(i * 512 + lane * 16)
+                     : uint32_t(chunk >> 3) * (BN * 128) + sw128(uint32_t(row), chunk & 7);
+            cp_async16(dst + at, src, live ? 16u : 0u);
+          }
+        }
+      };
+      // e4m3: this lane's staged pieces (16 codes each) to f16 in the tile
+      auto widen = [&](uint8_t* stage, uint8_t* dst) {
+#pragma unroll
+        for (int n = 0; n < C::NPL; ++n) {
+          const int i = li + kLoaders * n;
+          if (i < C::NI) {
+            const uint32_t row = i * C::RPI + sub;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 512 + lane * 16);
+            const uint2 a = e4m3x4_to_f16(w.x), b = e4m3x4_to_f16(w.y);
+            const uint2 c = e4m3x4_to_f16(w.z), d = e4m3x4_to_f16(w.w);
+            uint8_t* part = dst + uint32_t(chunk >> 2) * (BN * 128);
+            const uint32_t c0 = 2 * (chunk & 3);
+            *reinterpret_cast<uint4*>(part + sw128(row, c0)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(part + sw128(row, c0 + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+          }
+        }
+      };
+
+      bool more = next_unit(u_first), ok = true;
+      int t = nxt.t0;
+      int32_t e[C::NPL], en[C::NPL];
+      if (more) {
+        cur = nxt;
+        lookup(cur, t, e);
+        check(cur, t, e);
+      }
+      uint8_t* stage_k = smem + C::OFF_STAGE;
+      uint8_t* stage_v = stage_k + C::STAGE_BYTES;
+      const uint8_t* kc = nullptr;
+      const uint8_t* vc = nullptr;
+      auto set_head = [&](const Unit& x) {
+        kc = p.kc + size_t(x.kvh) * C::ROWB + chunk * 16;
+        vc = p.vc + size_t(x.kvh) * C::ROWB + chunk * 16;
+      };
+      if (more) set_head(cur);
+      if (E4M3 && more) {
+        copy_rows(kc, e, smem_u32(stage_k));
+        cp_async_commit();
+        copy_rows(vc, e, smem_u32(stage_v));
+        cp_async_commit();
+      }
+      uint32_t tc = 0, uc = 0;
+      while (more && ok) {
+        const bool first = t == cur.t0;
+        const Unit now = cur;
+        // the tile after this one, and its rows
+        t += BN;
+        if (t >= cur.t1) {
+          more = next_unit(u + 1);
+          if (more) {
+            cur = nxt;
+            t = cur.t0;
+          }
+        }
+        if (more) lookup(cur, t, en);
+        const int sk = tc % C::NSK, sv = tc % C::NSV;
+        ok = __all_sync(0xffffffffu, mbar_wait(k_empty + sk, ((tc / C::NSK) & 1) ^ 1, &abort_flag,
+                                               p.status));
+        if (!ok) break;
+        uint8_t* kdst = smem + C::OFF_K + sk * C::KV_BYTES;
+        uint8_t* vdst = smem + C::OFF_V + sv * C::KV_BYTES;
+        if constexpr (E4M3) {
+          cp_async_wait1();  // the older group: this tile's K
+          widen(stage_k, kdst);
+          fence_proxy_async_smem();
+          mbar_arrive(k_full + sk);
+          if (more) {
+            check(cur, t, en);
+            set_head(cur);
+            copy_rows(kc, en, smem_u32(stage_k));
+          }
+          cp_async_commit();
+        } else {
+          copy_rows(kc, e, smem_u32(kdst));
+          cp_async_arrive(k_full + sk);
+        }
+        if (first && warp == 0) {
+          if (lane == 0) {
+            ok = mbar_wait(q_empty, (uc & 1) ^ 1, &abort_flag, p.status);
+            if (ok) {
+              mbar_arrive_expect_tx(q_full, 2 * C::NPART * uint32_t(p.TPH) * p.G * 128);
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int part = 0; part < C::NPART; ++part)
+                  tma_load_3d(smem + C::OFF_Q + x * C::Q_BYTES + part * BM * 128, &tmap_q, q_full,
+                              part * 64, now.kvh * p.G, now.q0 + (now.twin ? 0 : x * p.TPH));
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, int(ok), 0);
+          if (!ok) break;
+        }
+        if (first) ++uc;
+        ok = __all_sync(0xffffffffu, mbar_wait(v_empty + sv, ((tc / C::NSV) & 1) ^ 1, &abort_flag,
+                                               p.status));
+        if (!ok) break;
+        if constexpr (E4M3) {
+          cp_async_wait1();  // the older group: this tile's V
+          widen(stage_v, vdst);
+          fence_proxy_async_smem();
+          mbar_arrive(v_full + sv);
+          if (more) copy_rows(vc, en, smem_u32(stage_v));
+          cp_async_commit();
+        } else {
+          copy_rows(vc, e, smem_u32(vdst));
+          cp_async_arrive(v_full + sv);
+          if (more) {
+            check(cur, t, en);
+            set_head(cur);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < C::NPL; ++n) e[n] = en[n];
+        ++tc;
+      }
+      // every copy this thread issued lands before the CTA can exit
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok || abort_flag) {
+        const uint64_t w0 = globaltimer();
+        while (globaltimer() - w0 < 1000000ull) {
+        }
+      }
+    } else if (lane == 0) {
+      // ================================================================ MMA issuer
+      const uint32_t idesc_qk = idesc_of<E4M3>(BM, BN, false);
+      const uint32_t idesc_pv = idesc_of<E4M3>(BM, D, true);
+      const uint32_t sQ = smem_u32(smem + C::OFF_Q);
+      const uint32_t sK = smem_u32(smem + C::OFF_K);
+      const uint32_t sV = smem_u32(smem + C::OFF_V);
+      uint32_t tc = 0, uc = 0;
+      uint32_t pvc[2] = {0, 0};  // PVs issued per half (all units)
+      uint32_t uhc[2] = {0, 0};  // units in which the half had work
+      bool ok = true;
+
+      auto wait_k = [&](uint32_t t) -> bool {
+        if (!mbar_wait(k_full + t % C::NSK, (t / C::NSK) & 1, &abort_flag, p.status)) return false;
+        fence_proxy_async_smem();  // the loaders' copies, before the MMA reads them
+        return true;
+      };
+      // S_X = Q_X K_t^T into the S columns of half x
+      auto issue_qk = [&](int x, uint32_t t) {
+        tc_fence_after();
+        const uint32_t qbase = sQ + x * C::Q_BYTES, kbase = sK + (t % C::NSK) * C::KV_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (BM * 128) + (ks & 3) * 32;
+          umma_ss(tmem + x * 256, umma_desc_sw128(qbase + off, 16, 1024),
+                  umma_desc_sw128(kbase + off, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full + x);
+      };
+      // O_X += P_X V_t, P_X in TMEM over the first 64 columns of S_X
+      auto issue_pv = [&](int x, uint32_t t, bool first) -> bool {
+        if (!mbar_wait(p_full + x, pvc[x] & 1, &abort_flag, p.status)) return false;
+        const int slot = t % C::NSV;
+        if (!mbar_wait(v_full + slot, (t / C::NSV) & 1, &abort_flag, p.status)) return false;
+        if (first && !mbar_wait(o_free + x, (uhc[x] & 1) ^ 1, &abort_flag, p.status)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t vbase = sV + slot * C::KV_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < BN / 16; ++ks)
+          umma_ts(tmem + x * 256 + 128, tmem + x * 256 + ks * 8,
+                  umma_desc_sw128(vbase + ks * 2048, BN * 128, 1024), idesc_pv,
+                  (first && ks == 0) ? 0u : 1u);
+        umma_commit(pv_done + x);
+        ++pvc[x];
+        return true;
+      };
+
+      for (int u = u_first; u < u_end && ok; ++u) {
+        const Unit w = load_unit(p, units, u);
+        if (!w.ok) continue;
+        const int n = (w.t1 - w.t0 + BN - 1) / BN;
+        if (!mbar_wait(E4M3 ? q_conv : q_full, uc & 1, &abort_flag, p.status)) break;
+        bool started[2] = {false, false};
+        bool see[2];
+        see[0] = half_sees(w, 0, w.t0, p.TPH, p.window);
+        see[1] = half_sees(w, 1, w.t0, p.TPH, p.window);
+        ok = wait_k(tc);
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (see[x]) issue_qk(x, tc);
+        umma_commit(k_empty + (tc % C::NSK));
+        if (n == 1) umma_commit(q_empty);
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t t = tc + j;
+          bool have_k = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ok && see[x]) {
+              ok = issue_pv(x, t, !started[x]);
+              started[x] = true;
+            }
+            see[x] = j + 1 < n && half_sees(w, x, w.t0 + (j + 1) * BN, p.TPH, p.window);
+            if (ok && see[x]) {
+              if (!have_k) ok = wait_k(t + 1);
+              have_k = true;
+              if (ok) issue_qk(x, t + 1);
+            }
+          }
+          if (!ok) break;
+          umma_commit(v_empty + (t % C::NSV));
+          if (j + 1 < n) {
+            umma_commit(k_empty + ((t + 1) % C::NSK));
+            if (j + 2 == n) umma_commit(q_empty);
+          }
+        }
+        if (!ok) break;
+        tc += n;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (started[x]) ++uhc[x];
+        ++uc;
+      }
+      if (!ok || abort_flag) {
+        // give MMAs already issued time to finish before TMEM is freed
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+    // ================================================================ softmax + epilogue
+    const int x = (warp - 4) >> 2;      // half
+    const int quarter = warp & 3;       // TMEM lane quarter
+    const int r = quarter * 32 + lane;  // row within the half
+    const int tok = r / p.G, g = r - tok * p.G;
+    const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16) + x * 256;
+    const uint32_t tS = trow, tO = trow + 128;
+    uint32_t sc_count = 0;  // S tiles of this half consumed (all units)
+    uint32_t uc = 0;
+    for (int u = u_first; u < u_end; ++u) {
+      const Unit w = load_unit(p, units, u);
+      if (!w.ok) continue;
+      if constexpr (E4M3) {
+        // widen this thread's query row to f16, in place
+        if (!mbar_wait(q_full, uc & 1, &abort_flag, p.status)) break;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(smem + C::OFF_Q + x * C::Q_BYTES +
+                                               (c >> 3) * (BM * 128) + sw128(r, c & 7));
+          const uint4 v = *at;
+          *at = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
+                           bf16x2_to_f16x2(v.w));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_conv);
+      }
+      ++uc;
+      const int ntok = half_tokens(w, x, p.TPH), pos_first = half_pos(w, x, p.TPH);
+      const bool valid = tok < p.TPH && tok < ntok;
+      const int pos = pos_first + tok;
+
+      float m_run = -INFINITY, l_run = 0.f;
+      int nt = 0;  // tiles of this half in this unit
+      bool ok = true;
+      for (int t = w.t0; t < w.t1; t += BN) {
+        if (!half_sees(w, x, t, p.TPH, p.window)) continue;
+        if (!mbar_wait(s_full + x, sc_count & 1, &abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+
+        // the whole S row in one TMEM load
+        uint32_t sr[BN];
+        tmem_ld128(tS, sr);
+        tmem_wait_ld();
+        // some row of the half does not see the whole tile
+        if (t + BN > w.t1 || t + BN - 1 > pos_first ||
+            (p.window && t <= pos_first + ntok - 1 - p.window)) {
+          uint32_t vis[4];
+          range_bits(vis, p.window ? max(pos - p.window + 1 - t, 0) : 0, min(pos + 1, w.t1) - t);
+#pragma unroll
+          for (int k = 0; k < BN; ++k)
+            if (!((vis[k >> 5] >> (k & 31)) & 1u)) sr[k] = __float_as_uint(-INFINITY);
+        }
+        // row max of the raw logits (scale and cap commute with max)
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(sr[k]);
+#pragma unroll
+        for (int k = 8; k < BN; ++k) mx8[k & 7] = fmaxf(mx8[k & 7], __uint_as_float(sr[k]));
+        float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        // c tanh(s / c) = c - 2 c / (1 + exp(2 s / c)), here in the log2
+        // domain: its error is absolute (a few 1e-7 c), as the weights need it
+        const float cap2 = -2.f * p.cap_log2;
+        if constexpr (CAP) {
+          if (mx != -INFINITY)
+            mx = fmaf(fast_rcp(1.f + fast_exp2(mx * p.scale_log2)), cap2, p.cap_log2);
+        } else {
+          mx *= p.scale_log2;
+        }
+        const float m_new = fmaxf(m_run, mx);
+        const bool resc = m_new > m_run + kRescaleLog2;
+        // O (the PVs of earlier tiles) is rescaled after P is stored, when the
+        // S row no longer occupies registers; it only has to happen before
+        // this tile's PV, which waits for p_full.
+        const bool rescale_o = __any_sync(0xffffffffu, resc) && nt > 0;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = fast_exp2(m_run - m_new);
+          l_run *= alpha;
+          m_run = m_new;
+        }
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+
+        // P over the S columns (masked logits are -inf and give exactly 0)
+        uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+        if constexpr (CAP) {
+          const float top = neg_m + p.cap_log2;
+#pragma unroll
+          for (int k = 0; k < BN / 2; ++k) {
+            const float s0 = __uint_as_float(sr[2 * k]), s1 = __uint_as_float(sr[2 * k + 1]);
+            const float r0 = fast_rcp(1.f + fast_exp2(s0 * p.scale_log2));
+            const float r1 = fast_rcp(1.f + fast_exp2(s1 * p.scale_log2));
+            const float p0 = s0 == -INFINITY ? 0.f : fast_exp2(fmaf(r0, cap2, top));
+            const float p1 = s1 == -INFINITY ? 0.f : fast_exp2(fmaf(r1, cap2, top));
+            acc2[k & 3] = f2_add(acc2[k & 3], f2_pack(p0, p1));
+            sr[k] = pack_p<E4M3>(p0, p1);
+          }
+        } else {
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
+#pragma unroll
+          for (int k = 0; k < BN / 2; ++k) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])),
+                             sc2, nm2),
+                      x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            acc2[k & 3] = f2_add(acc2[k & 3], f2_pack(p0, p1));
+            sr[k] = pack_p<E4M3>(p0, p1);  // into consumed registers (k <= 2k)
+          }
+        }
+        float ls8[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f2_unpack(acc2[k], ls8[2 * k], ls8[2 * k + 1]);
+        tmem_st64(tS, *reinterpret_cast<uint32_t(*)[BN / 2]>(sr));
+        l_run += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
+        if (rescale_o) {
+          // wait for the latest PV into O, then scale O by alpha in place
+          if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t rr[32];
+            tmem_ld32(tO + c * 32, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) rr[k] = __float_as_uint(__uint_as_float(rr[k]) * alpha);
+            tmem_st32(tO + c * 32, rr);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + x);
+        ++sc_count;
+        ++nt;
+      }
+      if (!ok) break;
+
+      // partial row of this thread's row in the block
+      const size_t prow = size_t(w.part) + (w.twin ? x * w.ntok * p.G : x * p.TPH * p.G) + r;
+      if (nt == 0) {
+        // no tile of this piece is this half's: an empty partial
+        if (valid && w.part >= 0) p.part_lse[prow] = -INFINITY;
+        continue;
+      }
+      // ---- epilogue: O / l straight from TMEM, LSE
+      if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) break;
+      tc_fence_after();
+      const float inv = l_run > 0.f ? p.v_scale / l_run : 0.f;
+      const float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+      const size_t row = size_t(w.q0 + (w.twin ? 0 : x * p.TPH) + tok) * p.Hq + w.kvh * p.G + g;
+      {
+        uint32_t orr[D];
+        if constexpr (D == 128) {
+          tmem_ld128(tO, orr);
+        } else {
+          tmem_ld64(tO, orr);
+        }
+        tmem_wait_ld();
+        if (valid) {
+          if (w.part >= 0) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D);
+#pragma unroll
+            for (int k = 0; k < D / 4; ++k)
+              dst[k] = make_float4(
+                  __uint_as_float(orr[4 * k]) * inv, __uint_as_float(orr[4 * k + 1]) * inv,
+                  __uint_as_float(orr[4 * k + 2]) * inv, __uint_as_float(orr[4 * k + 3]) * inv);
+            p.part_lse[prow] = lse2;
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              uint32_t o4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o4[i] = pack_bf16(__uint_as_float(orr[8 * k + 2 * i]) * inv,
+                                  __uint_as_float(orr[8 * k + 2 * i + 1]) * inv);
+              dst[k] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            }
+            if (p.lse) p.lse[row] = lse2 * kLn2;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free + x);
+    }
+  }
+
+  // ---- teardown: every role has finished issuing; free TMEM
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the partials of split blocks by their log2-sum-exp, one warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
+  constexpr int E = D / 32;
+  const ChunkPlanView view(p.n_ctas, p.n_units, p.n_joins);
+  if (__ldg(p.plan) != kChunkMagic || __ldg(p.plan + 1) != p.n_ctas ||
+      __ldg(p.plan + 2) != p.n_units || __ldg(p.plan + 3) != p.n_joins)
+    return;  // reported by the chunk kernel
+  const int4* join = reinterpret_cast<const int4*>(p.plan + view.joins + 8 * blockIdx.x);
+  const int4 a = __ldg(join);
+  const int count = __ldg(reinterpret_cast<const int32_t*>(join + 1));
+  const int q0 = a.x, rows = a.y, kvh = a.z;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  if (!psa_in_bounds(q0 >= 0 && rows > 0 && kvh >= 0 && kvh < p.Hkv && a.w >= 0 && count > 0 &&
+                         int64_t(q0) + (rows - 1) / p.G < p.n_rows &&
+                         a.w + int64_t(count) * rows <= p.part_rows,
+                     lane == 0 ? p.status : nullptr))
+    return;
+  const float* lse = p.part_lse + a.w + r;
+  float m = -INFINITY;
+  for (int i = lane; i < count; i += 32) m = fmaxf(m, lse[size_t(i) * rows]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const float* o0 = p.part_o + (size_t(a.w) + r) * D + lane * E;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int n = min(32, count - i0);
+    float wl = 0.f;
+    if (lane < n && m != -INFINITY) wl = fast_exp2(lse[size_t(i0 + lane) * rows] - m);
+    sum += wl;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wl, i);
+      if (w == 0.f) continue;  // an empty partial's rows were not written
+      const float* src = o0 + size_t(i0 + i) * rows * D;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const size_t row = size_t(q0 + r / p.G) * p.Hq + kvh * p.G + r % p.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Opt-in shared memory and the register count of one instantiation, looked up
+// once per device.
+template <int D, bool E4M3, bool CAP>
+int prepare_kernel(int dev) {
+  static std::atomic<uint64_t> done{0};
+  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return PSA_OK;
+  auto kern = chunk_kernel<D, E4M3, CAP>;
+  cudaFuncAttributes at;
+  if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return PSA_ERR_CUDA;
+  // setmaxnreg hands out what the launch reserved: fewer would never return
+  if (at.numRegs != kRegsLaunch) return PSA_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(Cfg<D, E4M3>::SMEM)) != cudaSuccess)
+    return PSA_ERR_CUDA;
+  if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return PSA_OK;
+}
+
+template <int D, bool E4M3, bool CAP>
+int launch_chunk_d(const ChunkArgs& a) {
+  using C = Cfg<D, E4M3>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PSA_ERR_CUDA;
+  int rc = prepare_kernel<D, E4M3, CAP>(dev);
+  if (rc != PSA_OK) return rc;
+  const int G = a.info.Hq / a.info.Hkv, TPH = BM / G;
+  CUtensorMap tq;
+  {
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(a.info.Hq), uint64_t(a.T)};
+    const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(a.info.Hq) * D * 2};
+    const uint32_t box[3] = {64u, uint32_t(G), uint32_t(TPH)};
+    rc = encode_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != PSA_OK) return rc;
+  }
+  Params p = {};
+  p.plan = a.plan;
+  p.n_ctas = a.info.n_ctas, p.n_units = a.info.n_units, p.n_joins = a.info.n_joins;
+  p.kc = static_cast<const uint8_t*>(a.kc);
+  p.vc = static_cast<const uint8_t*>(a.vc);
+  p.n_cache = a.n_cache;
+  p.kv_indices = a.kv_indices;
+  p.n_keys = a.info.n_keys;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.n_rows = a.info.n_rows, p.Hq = a.info.Hq, p.Hkv = a.info.Hkv, p.G = G, p.TPH = TPH;
+  p.window = a.info.window;
+  const float scale = a.scale * a.k_scale;
+  p.scale_log2 = CAP ? 2.f * kLog2e * scale / a.cap : scale * kLog2e;
+  p.cap_log2 = a.cap * kLog2e;
+  p.v_scale = a.v_scale;
+  p.part_o = a.part_o, p.part_lse = a.part_lse;
+  p.part_rows = a.info.part_rows;
+  p.status = a.status;
+  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, kThreads, C::SMEM, a.stream>>>(tq, p);
+  if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
+  if (a.info.n_joins > 0) {
+    const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 7) / 8);
+    chunk_join_kernel<D><<<grid, 256, 0, a.stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
+  }
+  return PSA_OK;
+}
+
+template <int D>
+int launch_chunk_of(const ChunkArgs& a) {
+  if (a.e4m3)
+    return a.cap > 0.f ? launch_chunk_d<D, true, true>(a) : launch_chunk_d<D, true, false>(a);
+  return a.cap > 0.f ? launch_chunk_d<D, false, true>(a) : launch_chunk_d<D, false, false>(a);
+}
+
+}  // namespace
+
+int launch_chunk(const ChunkArgs& a) {
+  switch (a.info.head_dim) {
+    case 64:
+      return launch_chunk_of<64>(a);
+    case 128:
+      return launch_chunk_of<128>(a);
+    default:
+      return PSA_ERR_UNSUPPORTED;
+  }
+}
+
+}  // namespace psa

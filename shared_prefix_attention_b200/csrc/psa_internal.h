@@ -138,4 +138,77 @@ struct SparseArgs {
 };
 int launch_sparse_latent(const SparseArgs& a);
 
+// ---------------------------------------------------------------- norm, rotation, cache rows
+
+struct RowsArgs {
+  const void* q;  // [T, Hq, D] rows at token stride q_stride (elements); nullable
+  const void* k;  // [T, Hkv, D]; nullable
+  const void* v;  // [T, Hkv, D], append only; nullable
+  int64_t q_stride, k_stride, v_stride;
+  bool f32;       // fp32 rows (bf16 otherwise)
+  int32_t T, Hq, Hkv, D;
+  psa_norm_rope how;
+  void* q_out;    // dense [T, Hq, D]; the backward: dq at its own token stride
+  void* k_out;    // dense [T, Hkv, D], dk, or (append) the key cache
+  void* v_out;    // append: the value cache
+  const int32_t* slots;  // append: cache row of every token (negative: none)
+  int64_t n_cache;
+  bool e4m3;             // append: caches hold e4m3
+  float k_scale, v_scale;
+  int32_t* status;
+  cudaStream_t stream;
+};
+int launch_rows(const RowsArgs& a);
+
+constexpr int kRowsBwdMaxBlocks = 4 * 148;
+struct RowsBwdArgs {
+  RowsArgs rows;         // q_out / k_out receive dq / dk
+  int64_t dq_stride, dk_stride;
+  const void* dq_out;    // upstream gradients of the outputs, dense
+  const void* dk_out;
+  float* part;           // [kRowsBwdMaxBlocks][2][D]
+  float* dq_weight;      // [D], nullable
+  float* dk_weight;
+};
+int launch_rows_bwd(const RowsBwdArgs& b);
+
+struct CacheReadArgs {
+  const void* kc;
+  const void* vc;
+  int64_t n_cache;
+  const int32_t* rows;
+  int64_t n;
+  int32_t Hkv, D;
+  bool e4m3;
+  float k_scale, v_scale;
+  void* k;
+  void* v;
+  int32_t* status;
+  cudaStream_t stream;
+};
+int launch_cache_read(const CacheReadArgs& a);
+
+// ---------------------------------------------------------------- chunk
+
+struct ChunkArgs {
+  const void* q;   // bf16 [n_rows, Hq, D]
+  const void* kc;  // bf16 or e4m3 [n_cache, Hkv, D]
+  const void* vc;
+  int64_t n_cache;
+  const int32_t* kv_indices;  // nullable: flat key position -> cache row
+  bool e4m3;
+  float k_scale, v_scale;
+  void* o;
+  float* lse;
+  int32_t T;       // rows of q
+  float scale, cap;
+  psa_chunk_info info;
+  const int32_t* plan;  // device copy of psa_build_chunk_plan's array
+  float* part_o;        // [part_rows][D]
+  float* part_lse;      // [part_rows], log2 domain
+  int32_t* status;
+  cudaStream_t stream;
+};
+int launch_chunk(const ChunkArgs& a);
+
 }  // namespace psa
