@@ -16,19 +16,27 @@
 // halves on one K/V tile stream, or, where the rows fit one half ("twin"),
 // with both halves on the same rows and alternate tiles: then each half keeps
 // its own running max and sum and writes its own partial.
-//   warps 0, 2, 3  loaders.  A page table scatters a tile's keys, so K and V
-//                  rows are gathered with 16-byte asynchronous copies straight
-//                  into the 128-byte-swizzled tiles the MMA reads (zero fill
-//                  behind the key range, so no unused cache row is touched).
-//                  e4m3 rows go through a thread-private staging area and are
-//                  widened to f16 (exact) by the thread that copied them.
-//                  Warp 0 also loads the query rows by TMA.
-//   warp 1         tcgen05 issuer: per half S = Q K^T into TMEM, O += P V with
-//                  P read from TMEM over the S columns.
-//   warps 4..11    softmax of the two halves, one row per thread, running max
-//                  in the log2 domain with lazy rescaling, and the epilogue:
-//                  final rows, or a partial (O / l and log2-sum-exp, fp32) for
-//                  the join kernel.
+//   warps 0, 2   loaders of K (and the query rows, by TMA) and of V.  A page
+//                table scatters a tile's keys, so their rows are gathered with
+//                16-byte asynchronous copies straight into the 128-byte-
+//                swizzled tiles the MMA reads, zeros behind the key range (no
+//                unused cache row is touched); whole tiles of a contiguous
+//                bf16 range come by TMA.  e4m3 rows go through a thread-
+//                private staging area and are widened to f16 (exact) by the
+//                thread that copied them.  The loaders share their schedulers
+//                with the softmax warps, which leave few issue slots: an
+//                earlier form that computed each copy's addresses took 7500
+//                cycles per tile where this one takes under 3000 (four-row
+//                TMA gathers move half as much as these copies: 21 against 41
+//                bytes per clock and SM).
+//   warp 1       tcgen05 issuer: per half S = Q K^T into TMEM, O += P V with P
+//                read from TMEM over the S columns.  The whole warp walks in
+//                step so that descriptors stay in uniform registers (a single
+//                lane in a divergent branch issued at half the rate).
+//   warps 4..11  softmax of the two halves, one row per thread, running max in
+//                the log2 domain with lazy rescaling, and the epilogue: final
+//                rows, or a partial (O / l and log2-sum-exp, fp32) for the
+//                join kernel.
 // P is rounded to bf16 (f16 over an e4m3 cache) for the tensor cores: at most
 // half a step per weight, averaged over the keys; the sum l keeps fp32.
 // Every wait is bounded.
@@ -51,15 +59,15 @@ namespace {
 constexpr int BM = 128;            // query rows per half
 constexpr int BN = kChunkTile;     // keys per tile
 constexpr int kThreads = 384;      // 12 warps
-constexpr int kLoaders = 3;        // warps 0, 2, 3
-constexpr float kRescaleLog2 = 8.f;
-constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
 // Registers: 384 threads x 168 at launch = 64512 = 128 x 104 (loaders, MMA)
 // + 256 x 200 (softmax: a whole 128-column S row in registers).  The launcher
 // checks the compiled count before the first launch.
 constexpr int kRegsLaunch = 168;
 constexpr int kRegsLow = 104, kRegsSoftmax = 200;
 static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr int kParts = 4;          // a loader makes a tile in four parts of 32 rows
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
 
 template <int D, bool E4M3>
 struct Cfg {
@@ -69,8 +77,8 @@ struct Cfg {
   static constexpr int ROWB = E4M3 ? D : 2 * D;    // bytes of a cached row
   static constexpr int CPR = ROWB / 16;            // 16-byte copies of a row
   static constexpr int RPI = 32 / CPR;             // rows per warp instruction
-  static constexpr int NI = BN / RPI;              // warp instructions per tile
-  static constexpr int NPL = (NI + kLoaders - 1) / kLoaders;  // ... of one loader
+  static constexpr int RG = 8 / RPI;               // instructions per 8 rows
+  static constexpr int NPP = BN / 8 * RG / kParts;  // instructions per part
   static constexpr uint32_t STAGE_BYTES = E4M3 ? BN * D : 0;  // raw K (or V) tile
   static constexpr int NSK = D == 64 ? 4 : (E4M3 ? 2 : 3);
   static constexpr int NSV = D == 64 ? 4 : 2;
@@ -139,9 +147,12 @@ __device__ __forceinline__ bool half_sees(const Unit& u, int x, int t, int TPH, 
   return t <= first + n - 1 && (window == 0 || min(t + BN, u.t1) - 1 > first - window);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(src_bytes)
+               "r"(live ? 16u : 0u)
                : "memory");
 }
 // Arrives on `bar` once every cp.async this thread issued so far has landed.
@@ -152,8 +163,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void cp_async_wait1() {
-  asm volatile("cp.async.wait_group 1;" ::: "memory");
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Four e4m3 codes to two f16 pairs (exact).
@@ -186,15 +198,36 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// Bits [a, b) of a 128-bit mask.
-__device__ __forceinline__ void range_bits(uint32_t (&m)[4], int a, int b) {
+// Logits outside [lo, hi) become -inf (their weights exactly 0).
+__device__ __forceinline__ void mask_row(uint32_t (&s)[BN], int lo, int hi) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int lo = min(max(a - 32 * w, 0), 32), hi = min(max(b - 32 * w, 0), 32);
-    const uint32_t below_hi = hi == 32 ? 0xffffffffu : ((1u << hi) - 1u);
-    const uint32_t below_lo = lo == 32 ? 0xffffffffu : ((1u << lo) - 1u);
-    m[w] = below_hi & ~below_lo;
+  for (int w = 0; w < BN / 32; ++w) {
+    const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+    const uint32_t below_b = b == 32 ? 0xffffffffu : ((1u << b) - 1u);
+    const uint32_t below_a = a == 32 ? 0xffffffffu : ((1u << a) - 1u);
+    const uint32_t keep = below_b & ~below_a;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (!((keep >> k) & 1u)) s[32 * w + k] = __float_as_uint(-INFINITY);
   }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max_of_row(const uint32_t (&s)[BN]) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(s[k]);
+#pragma unroll
+  for (int k = 8; k < BN - 8; k += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = max3(v[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 8 + i]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = max3(v[i], v[i + 4], __uint_as_float(s[BN - 8 + i]));
+  v[0] = max3(v[0], v[1], __uint_as_float(s[BN - 4]));
+  v[2] = max3(v[2], v[3], __uint_as_float(s[BN - 3]));
+  return max3(max3(v[0], v[2], __uint_as_float(s[BN - 2])), v[0],
+                  __uint_as_float(s[BN - 1]));
 }
 
 // kind::f16 with f16 or bf16 operands and fp32 accumulation.
@@ -204,9 +237,56 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t M, uint32_t N, bool b_m
          ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// The log2-domain logit of a raw one.  Capped: c tanh(s / c) = c - 2 c / (1 +
+// exp(2 s / c)); its error is absolute (a few 1e-7 c), as the weights need it.
+template <bool CAP>
+__device__ __forceinline__ float to_log2(float s, const Params& p) {
+  if constexpr (CAP)
+    return s == -INFINITY ? s
+                          : fmaf(fast_rcp(1.f + fast_exp2(s * p.scale_log2)), -2.f * p.cap_log2,
+                                 p.cap_log2);
+  else
+    return s * p.scale_log2;
+}
+
+// Weights of a row of logits against the max -neg_m, packed in pairs into the
+// row's first half (pair k over logit k <= 2 k, which is done by then);
+// returns their fp32 sum.
+template <bool F16, bool CAP>
+__device__ __forceinline__ float weights_row(uint32_t (&s)[BN], float neg_m, const Params& p) {
+  const float cap2 = -2.f * p.cap_log2, top = neg_m + p.cap_log2;
+  const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int k = 0; k < BN / 2; ++k) {
+    const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
+    float p0, p1;
+    if constexpr (CAP) {
+      const float r0 = fast_rcp(1.f + fast_exp2(s0 * p.scale_log2));
+      const float r1 = fast_rcp(1.f + fast_exp2(s1 * p.scale_log2));
+      p0 = s0 == -INFINITY ? 0.f : fast_exp2(fmaf(r0, cap2, top));
+      p1 = s1 == -INFINITY ? 0.f : fast_exp2(fmaf(r1, cap2, top));
+    } else {
+      const uint64_t x2 = f2_fma(f2_pack(s0, s1), sc2, nm2);
+      float x0, x1;
+      f2_unpack(x2, x0, x1);
+      p0 = fast_exp2(x0);
+      p1 = fast_exp2(x1);
+    }
+    acc[k & 3] = f2_add(acc[k & 3], f2_pack(p0, p1));
+    s[k] = pack_p<F16>(p0, p1);
+  }
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f2_unpack(acc[k], v[2 * k], v[2 * k + 1]);
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
 template <int D, bool E4M3, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, Params p) {
+    chunk_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                 const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, Params p) {
   using C = Cfg<D, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -246,11 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_conv, 8);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::NSK; ++i) {
-      mbar_init(k_full + i, kLoaders * 32);
+      mbar_init(k_full + i, 32);
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < C::NSV; ++i) {
-      mbar_init(v_full + i, kLoaders * 32);
+      mbar_init(v_full + i, 32);
       mbar_init(v_empty + i, 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -272,139 +352,159 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
-    if (warp != 1) {
+    if (warp == 0 || warp == 2) {
       // ================================================================ loaders
-      const int li = warp == 0 ? 0 : warp - 1;
+      // Warp 0 loads K (and the query rows), warp 2 loads V; the rings advance
+      // on their own.  A tile is made in four parts of 32 rows: of the groups
+      // of 8 rows, part v takes the RPI ones at (v % RG) * RPI.  A lane's rows
+      // of a part then all have the same place in the swizzle, so its copies
+      // differ by constant offsets, and one page-table entry per lane covers
+      // the part.
+      const bool is_k = warp == 0;
       const int sub = lane / C::CPR, chunk = lane % C::CPR;
-      if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_q);
-      int u = u_first;
-      Unit cur = {}, nxt = {};
-      auto next_unit = [&](int from) {
-        for (u = from; u < u_end; ++u) {
-          nxt = load_unit(p, units, u);
-          if (nxt.ok) return true;
-        }
-        return false;
-      };
-      // cache rows of this lane's copies of the tile at key t (-1: zeros)
-      auto lookup = [&](const Unit& x, int t, int32_t (&e)[C::NPL]) {
-#pragma unroll
-        for (int n = 0; n < C::NPL; ++n) {
-          const int i = li + kLoaders * n;
-          const int pos = t + i * C::RPI + sub;
-          e[n] = -1;
-          if (i < C::NI && pos < x.t1) {
-            const int64_t flat = int64_t(x.kv0) + pos;
-            e[n] = p.kv_indices ? __ldg(p.kv_indices + flat) : int32_t(flat);
-          }
-        }
-      };
-      auto check = [&](const Unit& x, int t, int32_t (&e)[C::NPL]) {
-#pragma unroll
-        for (int n = 0; n < C::NPL; ++n) {
-          const int i = li + kLoaders * n;
-          const bool live = i < C::NI && t + i * C::RPI + sub < x.t1;
-          if (live && (e[n] < 0 || e[n] >= p.n_cache)) {
-            report_status(p.status, PSA_ERR_INVALID_ARG);
-            e[n] = -1;
-          }
-        }
-      };
+      if (lane == 0) {
+        if (is_k) tma_prefetch_desc(&tmap_q);
+        if (!E4M3 && !p.kv_indices) tma_prefetch_desc(is_k ? &tmap_k : &tmap_v);
+      }
+      const uint8_t* cache = (is_k ? p.kc : p.vc) + chunk * 16;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      const uint32_t n_slots = is_k ? C::NSK : C::NSV;
+      uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+      uint8_t* stage = smem + C::OFF_STAGE + (is_k ? 0 : C::STAGE_BYTES) + lane * 16;
       const size_t row_bytes = size_t(p.Hkv) * C::ROWB;
-      // one tile of K or V: asynchronous copies of this lane's pieces, into
-      // the tile (bf16) or the staging area (e4m3)
-      auto copy_rows = [&](const uint8_t* cache, const int32_t (&e)[C::NPL], uint32_t dst) {
+      auto first_row = [](int v) { return v / C::RG * C::NPP * 8 + v % C::RG * C::RPI; };
+      const int lane_row = lane / C::RPI * 8 + lane % C::RPI;  // of a lane's table entry
+
+      int u = u_first - 1, t = 0;
+      Unit cur = {};  // the unit of the tile whose rows are at hand
+      bool more = true, all = false;
+      int32_t entry[kParts] = {};  // cache rows of this lane's table entries, -1: zeros
+      const uint8_t* head = nullptr;
+      // Moves on to the next tile and reads its page-table entries.
+      auto advance = [&]() {
+        t += BN;
+        if (u < u_first || t >= cur.t1) {
+          do {
+            if (++u >= u_end) {
+              more = false;
+              return;
+            }
+            cur = load_unit(p, units, u);
+          } while (!cur.ok);
+          t = cur.t0;
+          head = cache + size_t(cur.kvh) * C::ROWB;
+        }
 #pragma unroll
-        for (int n = 0; n < C::NPL; ++n) {
-          const int i = li + kLoaders * n;
-          if (i < C::NI) {
-            const int row = i * C::RPI + sub;
-            const bool live = e[n] >= 0;
-            const uint8_t* src = cache + size_t(live ? e[n] : 0) * row_bytes;
-            const uint32_t at =
-                E4M3 ? uint32_t(i * 512 + lane * 16)
-                     : uint32_t(chunk >> 3) * (BN * 128) + sw128(uint32_t(row), chunk & 7);
-            cp_async16(dst + at, src, live ? 16u : 0u);
+        for (int v = 0; v < kParts; ++v) {
+          const int pos = t + first_row(v) + lane_row;
+          entry[v] = -1;
+          if (pos < cur.t1) {
+            const int64_t flat = int64_t(cur.kv0) + pos;
+            entry[v] = p.kv_indices ? __ldg(p.kv_indices + flat) : int32_t(flat);
           }
         }
       };
-      // e4m3: this lane's staged pieces (16 codes each) to f16 in the tile
-      auto widen = [&](uint8_t* stage, uint8_t* dst) {
+      // Rows outside the cache become zeros and a report.
+      auto check = [&]() {
+        bool good = true;
 #pragma unroll
-        for (int n = 0; n < C::NPL; ++n) {
-          const int i = li + kLoaders * n;
-          if (i < C::NI) {
-            const uint32_t row = i * C::RPI + sub;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 512 + lane * 16);
-            const uint2 a = e4m3x4_to_f16(w.x), b = e4m3x4_to_f16(w.y);
-            const uint2 c = e4m3x4_to_f16(w.z), d = e4m3x4_to_f16(w.w);
-            uint8_t* part = dst + uint32_t(chunk >> 2) * (BN * 128);
-            const uint32_t c0 = 2 * (chunk & 3);
-            *reinterpret_cast<uint4*>(part + sw128(row, c0)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(part + sw128(row, c0 + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+        for (int v = 0; v < kParts; ++v) {
+          if (entry[v] < 0 || entry[v] >= p.n_cache) {
+            if (t + first_row(v) + lane_row < cur.t1) report_status(p.status, PSA_ERR_INVALID_ARG);
+            entry[v] = -1;
+            good = false;
           }
         }
+        all = __all_sync(0xffffffffu, good);
+      };
+      // one part: asynchronous copies of this lane's pieces, `step` bytes apart
+      auto copy_part = [&](int v, uint32_t dst, uint32_t step) {
+        if (all) {
+#pragma unroll
+          for (int n = 0; n < C::NPP; ++n)
+            cp_async16(dst + n * step,
+                       head + uint32_t(__shfl_sync(0xffffffffu, entry[v], n * C::RPI + sub)) *
+                                  row_bytes);
+        } else {
+#pragma unroll 1
+          for (int n = 0; n < C::NPP; ++n) {
+            const int32_t e = __shfl_sync(0xffffffffu, entry[v], n * C::RPI + sub);
+            cp_async16_or_zero(dst + n * step, head + size_t(max(e, 0)) * row_bytes, e >= 0);
+          }
+        }
+      };
+      // e4m3: this lane's staged pieces of a part (16 codes each) to f16
+      auto widen_part = [&](int v, uint8_t* dst) {
+        const uint32_t row = uint32_t(first_row(v) + sub), c0 = 2 * (chunk & 3);
+        dst += uint32_t(chunk >> 2) * (BN * 128);
+        uint8_t* at0 = dst + sw128(row, c0);
+        uint8_t* at1 = dst + sw128(row, c0 + 1);
+        const uint8_t* src = stage + v * C::NPP * 512;
+#pragma unroll
+        for (int n = 0; n < C::NPP; ++n) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src + n * 512);
+          const uint2 a = e4m3x4_to_f16(w.x), b = e4m3x4_to_f16(w.y);
+          const uint2 c = e4m3x4_to_f16(w.z), d = e4m3x4_to_f16(w.w);
+          *reinterpret_cast<uint4*>(at0 + n * 1024) = make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(at1 + n * 1024) = make_uint4(c.x, c.y, d.x, d.y);
+        }
+      };
+      auto stage_part = [&](int v) {
+        if (more) copy_part(v, smem_u32(stage) + v * C::NPP * 512, 512);
+        cp_async_commit();
       };
 
-      bool more = next_unit(u_first), ok = true;
-      int t = nxt.t0;
-      int32_t e[C::NPL], en[C::NPL];
-      if (more) {
-        cur = nxt;
-        lookup(cur, t, e);
-        check(cur, t, e);
-      }
-      uint8_t* stage_k = smem + C::OFF_STAGE;
-      uint8_t* stage_v = stage_k + C::STAGE_BYTES;
-      const uint8_t* kc = nullptr;
-      const uint8_t* vc = nullptr;
-      auto set_head = [&](const Unit& x) {
-        kc = p.kc + size_t(x.kvh) * C::ROWB + chunk * 16;
-        vc = p.vc + size_t(x.kvh) * C::ROWB + chunk * 16;
-      };
-      if (more) set_head(cur);
+      bool ok = true;
+      advance();
+      // the tile being made: whether there is one, and its unit's query rows
+      // when it is the unit's first (e4m3 runs a tile ahead with its copies)
+      bool now = more, first = true;
+      int4 qbox = make_int4(cur.q0, cur.kvh, cur.twin, 0);
       if (E4M3 && more) {
-        copy_rows(kc, e, smem_u32(stage_k));
-        cp_async_commit();
-        copy_rows(vc, e, smem_u32(stage_v));
-        cp_async_commit();
+        check();
+#pragma unroll
+        for (int v = 0; v < kParts; ++v) stage_part(v);
+        advance();
       }
-      uint32_t tc = 0, uc = 0;
-      while (more && ok) {
-        const bool first = t == cur.t0;
-        const Unit now = cur;
-        // the tile after this one, and its rows
-        t += BN;
-        if (t >= cur.t1) {
-          more = next_unit(u + 1);
-          if (more) {
-            cur = nxt;
-            t = cur.t0;
-          }
-        }
-        if (more) lookup(cur, t, en);
-        const int sk = tc % C::NSK, sv = tc % C::NSV;
-        ok = __all_sync(0xffffffffu, mbar_wait(k_empty + sk, ((tc / C::NSK) & 1) ^ 1, &abort_flag,
-                                               p.status));
+      uint32_t slot = 0, phase = 0, uc = 0;
+      while (now) {
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + slot, phase ^ 1, &abort_flag, p.status));
         if (!ok) break;
-        uint8_t* kdst = smem + C::OFF_K + sk * C::KV_BYTES;
-        uint8_t* vdst = smem + C::OFF_V + sv * C::KV_BYTES;
+        uint8_t* dst = ring + slot * C::KV_BYTES;
         if constexpr (E4M3) {
-          cp_async_wait1();  // the older group: this tile's K
-          widen(stage_k, kdst);
-          fence_proxy_async_smem();
-          mbar_arrive(k_full + sk);
-          if (more) {
-            check(cur, t, en);
-            set_head(cur);
-            copy_rows(kc, en, smem_u32(stage_k));
+          if (more) check();
+#pragma unroll
+          for (int v = 0; v < kParts; ++v) {
+            cp_async_wait<kParts - 1>();  // this part's copies, the oldest group
+            widen_part(v, dst);
+            stage_part(v);
           }
-          cp_async_commit();
+          fence_proxy_async_smem();
+          mbar_arrive(full + slot);
         } else {
-          copy_rows(kc, e, smem_u32(kdst));
-          cp_async_arrive(k_full + sk);
+          if (!p.kv_indices && t + BN <= cur.t1) {
+            // a whole tile of a contiguous range: one TMA copy
+            if (lane == 0) {
+              mbar_arrive_expect_tx(full + slot, C::KV_BYTES);
+#pragma unroll
+              for (int part = 0; part < C::NPART; ++part)
+                tma_load_3d(dst + part * BN * 128, is_k ? &tmap_k : &tmap_v, full + slot,
+                            part * 64, cur.kvh, cur.kv0 + t);
+            } else {
+              mbar_arrive(full + slot);
+            }
+          } else {
+            check();
+#pragma unroll
+            for (int v = 0; v < kParts; ++v)
+              copy_part(v, smem_u32(dst) + uint32_t(chunk >> 3) * (BN * 128) +
+                               sw128(uint32_t(first_row(v) + sub), chunk & 7), 1024);
+            cp_async_arrive(full + slot);
+          }
         }
-        if (first && warp == 0) {
+        if (first && is_k) {
+          // the query rows, behind the unit's first K tile
           if (lane == 0) {
             ok = mbar_wait(q_empty, (uc & 1) ^ 1, &abort_flag, p.status);
             if (ok) {
@@ -414,34 +514,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int part = 0; part < C::NPART; ++part)
                   tma_load_3d(smem + C::OFF_Q + x * C::Q_BYTES + part * BM * 128, &tmap_q, q_full,
-                              part * 64, now.kvh * p.G, now.q0 + (now.twin ? 0 : x * p.TPH));
+                              part * 64, qbox.y * p.G, qbox.x + (qbox.z ? 0 : x * p.TPH));
             }
           }
+          ++uc;
           ok = __shfl_sync(0xffffffffu, int(ok), 0);
           if (!ok) break;
         }
-        if (first) ++uc;
-        ok = __all_sync(0xffffffffu, mbar_wait(v_empty + sv, ((tc / C::NSV) & 1) ^ 1, &abort_flag,
-                                               p.status));
-        if (!ok) break;
         if constexpr (E4M3) {
-          cp_async_wait1();  // the older group: this tile's V
-          widen(stage_v, vdst);
-          fence_proxy_async_smem();
-          mbar_arrive(v_full + sv);
-          if (more) copy_rows(vc, en, smem_u32(stage_v));
-          cp_async_commit();
+          now = more;
+          first = more && t == cur.t0;
+          if (first) qbox = make_int4(cur.q0, cur.kvh, cur.twin, 0);
+          if (more) advance();
         } else {
-          copy_rows(vc, e, smem_u32(vdst));
-          cp_async_arrive(v_full + sv);
-          if (more) {
-            check(cur, t, en);
-            set_head(cur);
-          }
+          advance();
+          now = more;
+          first = more && t == cur.t0;
+          if (first) qbox = make_int4(cur.q0, cur.kvh, cur.twin, 0);
         }
-#pragma unroll
-        for (int n = 0; n < C::NPL; ++n) e[n] = en[n];
-        ++tc;
+        if (++slot == n_slots) slot = 0, phase ^= 1;
       }
       // every copy this thread issued lands before the CTA can exit
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -450,95 +541,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (globaltimer() - w0 < 1000000ull) {
         }
       }
-    } else if (lane == 0) {
+    } else if (warp == 1) {
       // ================================================================ MMA issuer
+      // The whole warp walks the units and waits (every value below is the
+      // same in all lanes, so descriptors and branches stay in uniform
+      // registers); one elected lane issues.
       const uint32_t idesc_qk = idesc_of<E4M3>(BM, BN, false);
       const uint32_t idesc_pv = idesc_of<E4M3>(BM, D, true);
-      const uint32_t sQ = smem_u32(smem + C::OFF_Q);
-      const uint32_t sK = smem_u32(smem + C::OFF_K);
-      const uint32_t sV = smem_u32(smem + C::OFF_V);
-      uint32_t tc = 0, uc = 0;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dQ = umma_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+      const uint64_t dK = umma_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+      const uint64_t dV = umma_desc_sw128(smem_u32(smem + C::OFF_V), BN * 128, 1024);
+      uint32_t sk = 0, kph = 0, sv = 0, vph = 0;  // ring slots of the next K / V tile
+      uint32_t uc = 0;
       uint32_t pvc[2] = {0, 0};  // PVs issued per half (all units)
       uint32_t uhc[2] = {0, 0};  // units in which the half had work
       bool ok = true;
 
-      auto wait_k = [&](uint32_t t) -> bool {
-        if (!mbar_wait(k_full + t % C::NSK, (t / C::NSK) & 1, &abort_flag, p.status)) return false;
-        fence_proxy_async_smem();  // the loaders' copies, before the MMA reads them
-        return true;
+      auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, &abort_flag, p.status));
       };
-      // S_X = Q_X K_t^T into the S columns of half x
-      auto issue_qk = [&](int x, uint32_t t) {
-        tc_fence_after();
-        const uint32_t qbase = sQ + x * C::Q_BYTES, kbase = sK + (t % C::NSK) * C::KV_BYTES;
+      // S_X = Q_X K^T into the S columns of half x
+      auto issue_qk = [&](int x) {
+        const uint64_t a = dQ + x * (C::Q_BYTES >> 4), b = dK + sk * (C::KV_BYTES >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * (BM * 128) + (ks & 3) * 32;
-          umma_ss(tmem + x * 256, umma_desc_sw128(qbase + off, 16, 1024),
-                  umma_desc_sw128(kbase + off, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4;
+            umma_ss(tm + x * 256, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(s_full + x);
         }
-        umma_commit(s_full + x);
       };
-      // O_X += P_X V_t, P_X in TMEM over the first 64 columns of S_X
-      auto issue_pv = [&](int x, uint32_t t, bool first) -> bool {
-        if (!mbar_wait(p_full + x, pvc[x] & 1, &abort_flag, p.status)) return false;
-        const int slot = t % C::NSV;
-        if (!mbar_wait(v_full + slot, (t / C::NSV) & 1, &abort_flag, p.status)) return false;
-        if (first && !mbar_wait(o_free + x, (uhc[x] & 1) ^ 1, &abort_flag, p.status)) return false;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t vbase = sV + slot * C::KV_BYTES;
+      // O_X += P_X V, P_X in TMEM over the first 64 columns of S_X
+      auto issue_pv = [&](int x, bool first) {
+        const uint64_t b = dV + sv * (C::KV_BYTES >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          umma_ts(tmem + x * 256 + 128, tmem + x * 256 + ks * 8,
-                  umma_desc_sw128(vbase + ks * 2048, BN * 128, 1024), idesc_pv,
-                  (first && ks == 0) ? 0u : 1u);
-        umma_commit(pv_done + x);
-        ++pvc[x];
-        return true;
+          for (int ks = 0; ks < BN / 16; ++ks)
+            umma_ts(tm + x * 256 + 128, tm + x * 256 + ks * 8, b + ks * (2048 >> 4), idesc_pv,
+                    (first && ks == 0) ? 0u : 1u);
+          umma_commit(pv_done + x);
+        }
+      };
+      auto commit = [&](uint64_t* b) {
+        if (elect_one()) umma_commit(b);
       };
 
-      for (int u = u_first; u < u_end && ok; ++u) {
+      const int last = __shfl_sync(0xffffffffu, u_end, 0);
+      for (int u = __shfl_sync(0xffffffffu, u_first, 0); u < last && ok; ++u) {
         const Unit w = load_unit(p, units, u);
         if (!w.ok) continue;
-        const int n = (w.t1 - w.t0 + BN - 1) / BN;
-        if (!mbar_wait(E4M3 ? q_conv : q_full, uc & 1, &abort_flag, p.status)) break;
+        const int n = __shfl_sync(0xffffffffu, (w.t1 - w.t0 + BN - 1) / BN, 0);
+        if (!wait(E4M3 ? q_conv : q_full, uc & 1)) {
+          ok = false;
+          break;
+        }
         bool started[2] = {false, false};
         bool see[2];
-        see[0] = half_sees(w, 0, w.t0, p.TPH, p.window);
-        see[1] = half_sees(w, 1, w.t0, p.TPH, p.window);
-        ok = wait_k(tc);
-        if (!ok) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (see[x]) issue_qk(x, tc);
-        umma_commit(k_empty + (tc % C::NSK));
-        if (n == 1) umma_commit(q_empty);
+          see[x] = __any_sync(0xffffffffu, half_sees(w, x, w.t0, p.TPH, p.window));
+        // the loaders' copies are ordered before the MMAs that read them
+        ok = wait(k_full + sk, kph);
+        if (!ok) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (see[x]) issue_qk(x);
+        commit(k_empty + sk);
+        if (n == 1) commit(q_empty);
+        if (++sk == C::NSK) sk = 0, kph ^= 1;
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t t = tc + j;
-          bool have_k = false;
+          bool have_k = false, have_v = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (ok && see[x]) {
-              ok = issue_pv(x, t, !started[x]);
+              ok = wait(p_full + x, pvc[x] & 1) && (have_v || wait(v_full + sv, vph)) &&
+                   (started[x] || wait(o_free + x, (uhc[x] & 1) ^ 1));
+              if (!ok) break;
+              if (!have_v) fence_proxy_async_smem();
+              have_v = true;
+              tc_fence_after();
+              issue_pv(x, !started[x]);
               started[x] = true;
+              ++pvc[x];
             }
-            see[x] = j + 1 < n && half_sees(w, x, w.t0 + (j + 1) * BN, p.TPH, p.window);
+            see[x] = j + 1 < n && __any_sync(0xffffffffu, half_sees(w, x, w.t0 + (j + 1) * BN,
+                                                                    p.TPH, p.window));
             if (ok && see[x]) {
-              if (!have_k) ok = wait_k(t + 1);
-              have_k = true;
-              if (ok) issue_qk(x, t + 1);
+              if (!have_k) {
+                ok = wait(k_full + sk, kph);
+                if (!ok) break;
+                fence_proxy_async_smem();
+                tc_fence_after();
+                have_k = true;
+              }
+              issue_qk(x);
             }
           }
           if (!ok) break;
-          umma_commit(v_empty + (t % C::NSV));
+          if (!have_v) ok = wait(v_full + sv, vph);
+          commit(v_empty + sv);
+          if (++sv == C::NSV) sv = 0, vph ^= 1;
           if (j + 1 < n) {
-            umma_commit(k_empty + ((t + 1) % C::NSK));
-            if (j + 2 == n) umma_commit(q_empty);
+            if (!have_k) ok = ok && wait(k_full + sk, kph);
+            commit(k_empty + sk);
+            if (j + 2 == n) commit(q_empty);
+            if (++sk == C::NSK) sk = 0, kph ^= 1;
           }
         }
         if (!ok) break;
-        tc += n;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (started[x]) ++uhc[x];
@@ -595,84 +709,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        // some row of the half does not see the whole tile
+        const bool masked = t + BN > w.t1 || t + BN - 1 > pos_first ||
+                            (p.window && t <= pos_first + ntok - 1 - p.window);
+        const int lo = p.window ? max(pos - p.window + 1 - t, 0) : 0;
+        const int hi = min(pos + 1, w.t1) - t;
 
         // the whole S row in one TMEM load
         uint32_t sr[BN];
         tmem_ld128(tS, sr);
         tmem_wait_ld();
-        // some row of the half does not see the whole tile
-        if (t + BN > w.t1 || t + BN - 1 > pos_first ||
-            (p.window && t <= pos_first + ntok - 1 - p.window)) {
-          uint32_t vis[4];
-          range_bits(vis, p.window ? max(pos - p.window + 1 - t, 0) : 0, min(pos + 1, w.t1) - t);
-#pragma unroll
-          for (int k = 0; k < BN; ++k)
-            if (!((vis[k >> 5] >> (k & 31)) & 1u)) sr[k] = __float_as_uint(-INFINITY);
-        }
-        // row max of the raw logits (scale and cap commute with max)
-        float mx8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(sr[k]);
-#pragma unroll
-        for (int k = 8; k < BN; ++k) mx8[k & 7] = fmaxf(mx8[k & 7], __uint_as_float(sr[k]));
-        float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        // c tanh(s / c) = c - 2 c / (1 + exp(2 s / c)), here in the log2
-        // domain: its error is absolute (a few 1e-7 c), as the weights need it
-        const float cap2 = -2.f * p.cap_log2;
-        if constexpr (CAP) {
-          if (mx != -INFINITY)
-            mx = fmaf(fast_rcp(1.f + fast_exp2(mx * p.scale_log2)), cap2, p.cap_log2);
-        } else {
-          mx *= p.scale_log2;
-        }
-        const float m_new = fmaxf(m_run, mx);
-        const bool resc = m_new > m_run + kRescaleLog2;
-        // O (the PVs of earlier tiles) is rescaled after P is stored, when the
-        // S row no longer occupies registers; it only has to happen before
-        // this tile's PV, which waits for p_full.
-        const bool rescale_o = __any_sync(0xffffffffu, resc) && nt > 0;
+        if (masked) mask_row(sr, lo, hi);
+        // lazy rescaling: the max is raised when it grew by more than 2^8.  O
+        // (the PVs of earlier tiles) is rescaled after P is stored, when the S
+        // row no longer occupies registers; it only has to happen before this
+        // tile's PV, which waits for p_full.
+        const float m_tile = to_log2<CAP>(max_of_row(sr), p);
         float alpha = 1.f;
-        if (resc) {
-          alpha = fast_exp2(m_run - m_new);
+        if (m_tile > m_run + kRescaleLog2) {
+          alpha = fast_exp2(m_run - m_tile);
           l_run *= alpha;
-          m_run = m_new;
+          m_run = m_tile;
         }
-        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-
-        // P over the S columns (masked logits are -inf and give exactly 0)
-        uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-        if constexpr (CAP) {
-          const float top = neg_m + p.cap_log2;
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            const float s0 = __uint_as_float(sr[2 * k]), s1 = __uint_as_float(sr[2 * k + 1]);
-            const float r0 = fast_rcp(1.f + fast_exp2(s0 * p.scale_log2));
-            const float r1 = fast_rcp(1.f + fast_exp2(s1 * p.scale_log2));
-            const float p0 = s0 == -INFINITY ? 0.f : fast_exp2(fmaf(r0, cap2, top));
-            const float p1 = s1 == -INFINITY ? 0.f : fast_exp2(fmaf(r1, cap2, top));
-            acc2[k & 3] = f2_add(acc2[k & 3], f2_pack(p0, p1));
-            sr[k] = pack_p<E4M3>(p0, p1);
-          }
-        } else {
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])),
-                             sc2, nm2),
-                      x0, x1);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            acc2[k & 3] = f2_add(acc2[k & 3], f2_pack(p0, p1));
-            sr[k] = pack_p<E4M3>(p0, p1);  // into consumed registers (k <= 2k)
-          }
-        }
-        float ls8[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f2_unpack(acc2[k], ls8[2 * k], ls8[2 * k + 1]);
+        l_run += weights_row<E4M3, CAP>(sr, m_run == -INFINITY ? 0.f : -m_run, p);
         tmem_st64(tS, *reinterpret_cast<uint32_t(*)[BN / 2]>(sr));
-        l_run += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
-        if (rescale_o) {
+        if (nt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // wait for the latest PV into O, then scale O by alpha in place
           if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) {
             ok = false;
@@ -708,41 +769,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l straight from TMEM, LSE
       if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) break;
       tc_fence_after();
-      const float inv = l_run > 0.f ? p.v_scale / l_run : 0.f;
-      const float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+      const float inv = l_run == 0.f ? 0.f : p.v_scale / l_run;
+      const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
       const size_t row = size_t(w.q0 + (w.twin ? 0 : x * p.TPH) + tok) * p.Hq + w.kvh * p.G + g;
-      {
-        uint32_t orr[D];
-        if constexpr (D == 128) {
-          tmem_ld128(tO, orr);
-        } else {
-          tmem_ld64(tO, orr);
-        }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t orr[32];
+        tmem_ld32(tO + c * 32, orr);
         tmem_wait_ld();
-        if (valid) {
-          if (w.part >= 0) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D);
+        if (valid && w.part >= 0) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
-            for (int k = 0; k < D / 4; ++k)
-              dst[k] = make_float4(
-                  __uint_as_float(orr[4 * k]) * inv, __uint_as_float(orr[4 * k + 1]) * inv,
-                  __uint_as_float(orr[4 * k + 2]) * inv, __uint_as_float(orr[4 * k + 3]) * inv);
-            p.part_lse[prow] = lse2;
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D);
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(
+                __uint_as_float(orr[4 * k]) * inv, __uint_as_float(orr[4 * k + 1]) * inv,
+                __uint_as_float(orr[4 * k + 2]) * inv, __uint_as_float(orr[4 * k + 3]) * inv);
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c * 32);
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-              uint32_t o4[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o4[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o4[i] = pack_bf16(__uint_as_float(orr[8 * k + 2 * i]) * inv,
-                                  __uint_as_float(orr[8 * k + 2 * i + 1]) * inv);
-              dst[k] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-            }
-            if (p.lse) p.lse[row] = lse2 * kLn2;
+            for (int i = 0; i < 4; ++i)
+              o4[i] = pack_bf16(__uint_as_float(orr[8 * k + 2 * i]) * inv,
+                                __uint_as_float(orr[8 * k + 2 * i + 1]) * inv);
+            dst[k] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
           }
         }
       }
+      if (valid && w.part >= 0) p.part_lse[prow] = lse2;
+      if (valid && w.part < 0 && p.lse) p.lse[row] = lse2 * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free + x);
@@ -849,6 +905,18 @@ int launch_chunk_d(const ChunkArgs& a) {
                      CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc != PSA_OK) return rc;
   }
+  CUtensorMap tk = tq, tv = tq;  // only read for a contiguous bf16 range
+  if (!E4M3 && !a.kv_indices) {
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(a.info.Hkv), uint64_t(a.n_cache)};
+    const uint64_t strides[2] = {uint64_t(D) * 2, uint64_t(a.info.Hkv) * D * 2};
+    const uint32_t box[3] = {64u, 1u, uint32_t(BN)};
+    rc = encode_tmap(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.kc, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != PSA_OK) return rc;
+    rc = encode_tmap(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.vc, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != PSA_OK) return rc;
+  }
   Params p = {};
   p.plan = a.plan;
   p.n_ctas = a.info.n_ctas, p.n_units = a.info.n_units, p.n_joins = a.info.n_joins;
@@ -868,7 +936,7 @@ int launch_chunk_d(const ChunkArgs& a) {
   p.part_o = a.part_o, p.part_lse = a.part_lse;
   p.part_rows = a.info.part_rows;
   p.status = a.status;
-  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, kThreads, C::SMEM, a.stream>>>(tq, p);
+  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, kThreads, C::SMEM, a.stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   if (a.info.n_joins > 0) {
     const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 7) / 8);
