@@ -12,12 +12,15 @@
 // and cache_read copies cache rows back to dense bf16 (e4m3 * scale).
 //
 // All of it is bound by memory: each input element is read once and each
-// output element written once, in 16-byte lane accesses, with everything in
-// between in fp32 registers and one rounding at the store.  A row is spread
-// over d/8 lanes of 8 elements, so the norm's sum is log2(d/8) shuffles and
-// the half-split rotation fetches its partner elements from the lane rot/16
-// away.  A warp keeps one token's cos/sin and weights in registers over all
-// the heads of its task.
+// output element written once, with everything in between in fp32 registers
+// and one rounding at the store.  A row is spread over d/16 lanes of two
+// 8-element pieces each.  In the half-split form a lane's pieces are partners
+// of one another (pairs (i, i + rot/2)), in the interleaved form they are
+// neighbours, so a rotation never leaves its lane; the norm's sum is
+// log2(d/16) shuffles.  (One piece per lane, partners exchanged by eight
+// shuffles a row, took two to three times as long.)  A warp keeps one token's
+// cos/sin and weights in registers over the heads of its task and has kUnroll
+// row groups' loads in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -30,121 +33,141 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kUnroll = 4;  // rows a lane group has in flight
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane's share of a row as it was loaded: two pieces of 8 elements.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  static constexpr int kUnroll = 4;  // row groups in flight
+  uint4 v[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int a, int b) {
+    v[0] = *reinterpret_cast<const uint4*>(row + a);
+    v[1] = *reinterpret_cast<const uint4*>(row + b);
+  }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
+        x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  static constexpr int kUnroll = 2;
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* row, int a, int b) {
+    v[0] = reinterpret_cast<const float4*>(row + a)[0];
+    v[1] = reinterpret_cast<const float4*>(row + a)[1];
+    v[2] = reinterpret_cast<const float4*>(row + b)[0];
+    v[3] = reinterpret_cast<const float4*>(row + b)[1];
+  }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[4 * j] = v[j].x, x[4 * j + 1] = v[j].y, x[4 * j + 2] = v[j].z, x[4 * j + 3] = v[j].w;
+  }
+};
+
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int a, int b, const float (&x)[16]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float* y = x + 8 * j;
+    *reinterpret_cast<uint4*>(row + (j ? b : a)) =
+        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                   pack_bf16(y[6], y[7]));
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0];
-  const float4 b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-// e4m3(x / scale), saturating at +-448 (NaN stays NaN).  The division is the
-// exact one, so the code equals the rounding of the fp32 quotient.
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
-  uint32_t w[2];
+__device__ __forceinline__ void store_row(float* row, int a, int b, const float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)), __NV_SATFINITE,
-        __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)),
-        __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | (hi << 16);
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<float4*>(row + (j < 2 ? a : b))[j & 1] =
+        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+}
+// e4m3(x * inv), inv = 1 / scale in fp32 (a step of fp32 from the quotient at
+// most), saturating at +-448 (NaN stays NaN).
+__device__ __forceinline__ void store_row_e4m3(uint8_t* row, int a, int b, const float (&x)[16],
+                                               float inv) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* y = x + 8 * j + 4 * i;
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(row + (j ? b : a)) = make_uint2(w[0], w[1]);
   }
-  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// Sum over the LPR lanes of a row group (every lane gets it).
+// Sum over the LPR lanes of a row (every lane gets it).
 template <int LPR>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
 
-// One lane's share of a token's rotation.  Half-split form: the lane's 8
-// elements pair with those of lane `src`, by 8 angles; interleaved form: 4
-// pairs inside the lane.  `s` carries the sign of the lane's half, so both
-// halves compute own * c + other * s.  Lanes behind rot (on == false) keep
-// their elements, infinities included.
-template <bool INTER>
-struct Turn {
-  float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
-  int src;
+// Where a lane's two pieces start.  Lanes before rot/16 hold the rotated
+// elements: partners (half-split) or 16 neighbours (interleaved).  The others
+// pass their 16 neighbours through, infinities included.
+struct Pieces {
+  int a, b;
   bool on;
 };
-
 template <bool INTER>
-__device__ __forceinline__ void load_turn(Turn<INTER>& t, const float* cos_sin, int rot, int l,
-                                          int lane, float dir) {
-  constexpr int N = INTER ? 4 : 8;
-  t.src = lane;
-  t.on = 8 * l < rot;
+__device__ __forceinline__ Pieces pieces_of(int l, int rot) {
+  Pieces s;
+  s.on = 16 * l < rot;
+  s.a = 16 * l, s.b = s.a + 8;
+  if (!INTER && s.on) s.a = 8 * l, s.b = rot / 2 + 8 * l;
+  return s;
+}
+
+// The lane's eight angles of one position; dir -1 turns back.
+__device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const float* cos_sin,
+                                          int rot, int l, float dir) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) t.c[i] = 1.f, t.s[i] = 0.f;
-  if (!t.on) return;
-  const int half = rot / 2;
-  int a0;  // first angle of the lane
-  float sign;
-  if constexpr (INTER) {
-    a0 = 4 * l;
-    sign = dir;
-  } else {
-    const bool first = 8 * l < half;
-    a0 = first ? 8 * l : 8 * l - half;
-    t.src = first ? lane + half / 8 : lane - half / 8;
-    sign = first ? -dir : dir;
+  for (int i = 0; i < 8; i += 4) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(cos_sin + 8 * l + i));
+    const float4 y = __ldg(reinterpret_cast<const float4*>(cos_sin + rot / 2 + 8 * l + i));
+    c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+    s[i] = dir * y.x, s[i + 1] = dir * y.y, s[i + 2] = dir * y.z, s[i + 3] = dir * y.w;
   }
+}
+template <bool INTER>
+__device__ __forceinline__ void turn_row(const float (&c)[8], const float (&s)[8],
+                                         float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cos_sin + a0 + i));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(cos_sin + half + a0 + i));
-    t.c[i] = c.x, t.c[i + 1] = c.y, t.c[i + 2] = c.z, t.c[i + 3] = c.w;
-    t.s[i] = sign * s.x, t.s[i + 1] = sign * s.y, t.s[i + 2] = sign * s.z, t.s[i + 3] = sign * s.w;
+  for (int i = 0; i < 8; ++i) {
+    float& a = x[INTER ? 2 * i : i];
+    float& b = x[INTER ? 2 * i + 1 : 8 + i];
+    const float a0 = a, b0 = b;
+    a = a0 * c[i] - b0 * s[i];
+    b = a0 * s[i] + b0 * c[i];
   }
 }
 
-template <bool INTER>
-__device__ __forceinline__ void turn8(const Turn<INTER>& t, float (&x)[8]) {
-  if constexpr (INTER) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = t.on ? a * t.c[i] - b * t.s[i] : a;
-      x[2 * i + 1] = t.on ? a * t.s[i] + b * t.c[i] : b;
-    }
+__device__ __forceinline__ void load_weight(const void* w, int dtype, const Pieces& pc,
+                                            float (&x)[16]) {
+  if (dtype == PSA_F32) {
+    Raw<float> r;
+    r.load(static_cast<const float*>(w), pc.a, pc.b);
+    r.get(x);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, x[i], t.src);
-      x[i] = t.on ? x[i] * t.c[i] + other * t.s[i] : x[i];
-    }
+    Raw<__nv_bfloat16> r;
+    r.load(static_cast<const __nv_bfloat16*>(w), pc.a, pc.b);
+    r.get(x);
   }
-}
-
-__device__ __forceinline__ void load_weight(const void* w, int dtype, int l, float (&x)[8]) {
-  if (dtype == PSA_F32)
-    load8(static_cast<const float*>(w) + 8 * l, x);
-  else
-    load8(static_cast<const __nv_bfloat16*>(w) + 8 * l, x);
 }
 
 struct RowParams {
@@ -166,12 +189,13 @@ struct RowParams {
   const int32_t* slots;  // append form: cache row per token, negative: none
   int64_t n_cache;
   bool e4m3;
-  float scale[2];        // k_scale, v_scale
+  float inv_scale[2];    // of k_scale, v_scale
   int32_t* status;
   // backward
   const void* dy[2];     // upstream gradients, dense
   int64_t dxs[2];        // token strides of dx (in y[0], y[1])
-  float* part;           // [grid][2][D] partial weight gradients
+  float* part;           // [grid][D] partial weight gradients
+  int32_t blocks_q;      // the blocks below it work on q, the others on k
 };
 
 // The token's row in the angle table; -1 (and a report) if it is outside.
@@ -200,10 +224,10 @@ __device__ __forceinline__ Task task_of(const RowParams& p, int64_t task) {
   return k;
 }
 
-// Forward and append: one warp per task, its rows kUnroll at a time.
+// Forward and append: one warp per task, its row groups kUnroll at a time.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
-  constexpr int LPR = D / 8, GROUPS = 32 / LPR;
+  constexpr int LPR = D / 16, GROUPS = 32 / LPR, U = Raw<T>::kUnroll;
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
   const int64_t task = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (task >= int64_t(p.T) * p.nslice) return;
@@ -221,151 +245,159 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
   }
   const int64_t at = token_angle(p, k.t, lane);
   if (at < 0) return;
-  const bool turns = p.rot > 0 && k.kind < 2;
   const bool norms = k.kind < 2 && p.w[k.kind] != nullptr;
-  Turn<INTER> turn;
-  if (turns) load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, lane, 1.f);
-  float w[8];
-  if (norms) load_weight(p.w[k.kind], p.w_dtype, l, w);
-  const T* x0 = static_cast<const T*>(p.x[k.kind]) + int64_t(k.t) * p.xs[k.kind] + 8 * l;
+  const Pieces pc = pieces_of<INTER>(l, k.kind < 2 ? p.rot : 0);
+  float c[8], s[8], w[16];
+  if (pc.on) load_turn(c, s, p.cos_sin + at * p.rot, p.rot, l, 1.f);
+  if (norms) load_weight(p.w[k.kind], p.w_dtype, pc, w);
+  const T* x0 = static_cast<const T*>(p.x[k.kind]) + int64_t(k.t) * p.xs[k.kind];
   const size_t y0 = size_t(out_row) * p.H[k.kind];
 
-  for (int hb = k.h0; hb < k.h1; hb += GROUPS * kUnroll) {
-    float x[kUnroll][8];
+  for (int hb = k.h0; hb < k.h1; hb += GROUPS * U) {
+    Raw<T> raw[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int h = hb + u * GROUPS + g;
-      if (h < k.h1) load8(x0 + size_t(h) * D, x[u]);
+      if (h < k.h1) raw[u].load(x0 + size_t(h) * D, pc.a, pc.b);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int h = hb + u * GROUPS + g;
       if (hb + u * GROUPS >= k.h1) break;  // uniform: every lane takes part in the shuffles
+      float x[16];
+      raw[u].get(x);
       if (norms) {
-        float ss = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-        const float r = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + p.eps);
+        for (int i = 0; i < 8; ++i) {
+          s0 = fmaf(x[i], x[i], s0);
+          s1 = fmaf(x[8 + i], x[8 + i], s1);
+        }
+        const float r = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] *= r * w[i];
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
       }
-      if (turns) turn8<INTER>(turn, x[u]);
+      if (pc.on) turn_row<INTER>(c, s, x);
       if (h >= k.h1) continue;
-      const size_t off = (y0 + h) * D + 8 * l;
+      const size_t off = (y0 + h) * D;
       if (k.kind > 0 && p.e4m3)
-        store8_e4m3(static_cast<uint8_t*>(p.y[k.kind]) + off, x[u], p.scale[k.kind - 1]);
+        store_row_e4m3(static_cast<uint8_t*>(p.y[k.kind]) + off, pc.a, pc.b, x,
+                       p.inv_scale[k.kind - 1]);
       else
-        store8(static_cast<T*>(p.y[k.kind]) + off, x[u]);
+        store_row(static_cast<T*>(p.y[k.kind]) + off, pc.a, pc.b, x);
     }
   }
 }
 
-// Backward: a fixed grid strides over the tasks, so that each block sums its
-// rows' weight gradients in registers and writes one partial; the order of
-// every sum is fixed by the sizes alone.
+// Backward: every block works on one kind and strides over its tasks, so that
+// it sums its rows' weight gradients in registers and writes one partial; the
+// order of every sum is fixed by the sizes alone.
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kRowThreads) rows_bwd_kernel(RowParams p) {
-  constexpr int LPR = D / 8, GROUPS = 32 / LPR, U = 2;
-  __shared__ float red[kRowWarps][2][D];
+__global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
+  constexpr int LPR = D / 16, GROUPS = 32 / LPR, U = Raw<T>::kUnroll / 2;
+  __shared__ float red[kRowWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, g = lane / LPR;
-  float dw[2][8];
+  const int kind = int(blockIdx.x) < p.blocks_q ? 0 : 1;
+  const int block = int(blockIdx.x) - (kind ? p.blocks_q : 0);
+  const int blocks = kind ? int(gridDim.x) - p.blocks_q : p.blocks_q;
+  const Pieces pc = pieces_of<INTER>(l, p.rot);
+  const bool norms = p.w[kind] != nullptr;
+  const int H = p.H[kind], slices = p.slices[kind];
+  float w[16], dw[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-  const int64_t tasks = int64_t(p.T) * p.nslice;
-  for (int64_t task = int64_t(blockIdx.x) * kRowWarps + warp; task < tasks;
-       task += int64_t(gridDim.x) * kRowWarps) {
-    const Task k = task_of(p, task);
-    const int64_t at = token_angle(p, k.t, lane);
+  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  if (norms) load_weight(p.w[kind], p.w_dtype, pc, w);
+  const int64_t tasks = int64_t(p.T) * slices;
+  for (int64_t task = int64_t(block) * kRowWarps + warp; task < tasks;
+       task += int64_t(blocks) * kRowWarps) {
+    const int t = int(task / slices);
+    const int h0 = int(task - int64_t(t) * slices) * p.hs, h1 = min(h0 + p.hs, H);
+    const int64_t at = token_angle(p, t, lane);
     if (at < 0) continue;
-    Turn<INTER> turn;
-    if (p.rot) load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, lane, -1.f);
-    const bool norms = p.w[k.kind] != nullptr;
-    float w[8];
-    if (norms) load_weight(p.w[k.kind], p.w_dtype, l, w);
-    const T* x0 = static_cast<const T*>(p.x[k.kind]) + int64_t(k.t) * p.xs[k.kind] + 8 * l;
-    const T* g0 = static_cast<const T*>(p.dy[k.kind]) + int64_t(k.t) * p.H[k.kind] * D + 8 * l;
-    T* d0 = static_cast<T*>(p.y[k.kind]) + int64_t(k.t) * p.dxs[k.kind] + 8 * l;
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int hb = k.h0; hb < k.h1; hb += GROUPS * U) {
-      float x[U][8], dy[U][8];
+    float c[8], s[8];
+    if (pc.on) load_turn(c, s, p.cos_sin + at * p.rot, p.rot, l, -1.f);
+    const T* x0 = static_cast<const T*>(p.x[kind]) + int64_t(t) * p.xs[kind];
+    const T* g0 = static_cast<const T*>(p.dy[kind]) + int64_t(t) * H * D;
+    T* d0 = static_cast<T*>(p.y[kind]) + int64_t(t) * p.dxs[kind];
+    for (int hb = h0; hb < h1; hb += GROUPS * U) {
+      Raw<T> xr[U], gr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = hb + u * GROUPS + g;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = dy[u][i] = 0.f;
-        if (h < k.h1) {
-          load8(g0 + size_t(h) * D, dy[u]);
-          if (norms) load8(x0 + size_t(h) * D, x[u]);
+        // rows behind the last one: zeros, they add nothing to the sums
+        xr[u] = Raw<T>{};
+        gr[u] = Raw<T>{};
+        if (h < h1) {
+          gr[u].load(g0 + size_t(h) * D, pc.a, pc.b);
+          if (norms) xr[u].load(x0 + size_t(h) * D, pc.a, pc.b);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = hb + u * GROUPS + g;
-        if (hb + u * GROUPS >= k.h1) break;
-        if (p.rot) turn8<INTER>(turn, dy[u]);
+        if (hb + u * GROUPS >= h1) break;
+        float dy[16];
+        gr[u].get(dy);
+        if (pc.on) turn_row<INTER>(c, s, dy);
         if (norms) {
+          float x[16];
+          xr[u].get(x);
           float ss = 0.f, dot = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(x[u][i], x[u][i], ss);
-            dot = fmaf(w[i] * dy[u][i], x[u][i], dot);
+          for (int i = 0; i < 16; ++i) {
+            ss = fmaf(x[i], x[i], ss);
+            dot = fmaf(w[i] * dy[i], x[i], dot);
           }
-          ss = group_sum<LPR>(ss);
-          dot = group_sum<LPR>(dot);
+          ss = row_sum<LPR>(ss);
+          dot = row_sum<LPR>(dot);
           const float r = rsqrtf(ss * (1.f / D) + p.eps);
-          const float c = r * r * dot * (1.f / D);
+          const float e = r * r * dot * (1.f / D);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[i] = fmaf(dy[u][i], x[u][i] * r, acc[i]);
-            dy[u][i] = r * (w[i] * dy[u][i] - x[u][i] * c);
+          for (int i = 0; i < 16; ++i) {
+            dw[i] = fmaf(dy[i], x[i] * r, dw[i]);
+            dy[i] = r * (w[i] * dy[i] - x[i] * e);
           }
         }
-        if (h < k.h1) store8(d0 + size_t(h) * D, dy[u]);
+        if (h < h1) store_row(d0 + size_t(h) * D, pc.a, pc.b, dy);
       }
-    }
-    // a selection, not an index: dw stays in registers
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dw[0][i] += k.kind == 0 ? acc[i] : 0.f;
-      dw[1][i] += k.kind == 1 ? acc[i] : 0.f;
     }
   }
   // the row groups of a warp, then the warps of the block
 #pragma unroll
-  for (int kd = 0; kd < 2; ++kd)
+  for (int i = 0; i < 16; ++i) {
+    float v = dw[i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = dw[kd][i];
-#pragma unroll
-      for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (g == 0) red[warp][kd][8 * l + i] = v;
-    }
+    for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (g == 0) red[warp][(i < 8 ? pc.a : pc.b) + (i & 7)] = v;
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kRowThreads) {
+  for (int i = threadIdx.x; i < D; i += kRowThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int wi = 0; wi < kRowWarps; ++wi) v += (&red[wi][0][0])[i];
-    p.part[size_t(blockIdx.x) * 2 * D + i] = v;
+    for (int wi = 0; wi < kRowWarps; ++wi) v += red[wi][i];
+    p.part[size_t(blockIdx.x) * D + i] = v;
   }
 }
 
-// Sums the blocks' partials: one block per 32 weights, eight strided partial
-// sums per weight, joined in shared memory in a fixed order.
-__global__ void __launch_bounds__(256) weight_sum_kernel(const float* part, int nblocks, int D,
-                                                         float* dqw, float* dkw) {
+// Sums the blocks' partials, [0, blocks_q) for q and the rest for k: one block
+// per 32 weights, eight strided partial sums per weight, joined in shared
+// memory in a fixed order.
+__global__ void __launch_bounds__(256) weight_sum_kernel(const float* part, int blocks_q,
+                                                         int blocks, int D, float* dqw,
+                                                         float* dkw) {
   __shared__ float red[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
+  const int kind = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
+  const int b0 = kind ? blocks_q : 0, b1 = kind ? blocks : blocks_q;
   float v = 0.f;
-  for (int b = j; b < nblocks; b += 8) v += part[size_t(b) * 2 * D + c];
+#pragma unroll 4
+  for (int b = b0 + j; b < b1; b += 8) v += part[size_t(b) * D + c];
   red[j][threadIdx.x & 31] = v;
   __syncthreads();
   if (j == 0) {
 #pragma unroll
     for (int i = 1; i < 8; ++i) v += red[i][threadIdx.x & 31];
-    float* dst = c < D ? dqw : dkw;
-    if (dst) dst[c < D ? c : c - D] = v;
+    float* dst = kind ? dkw : dqw;
+    if (dst) dst[c] = v;
   }
 }
 
@@ -419,7 +451,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(
 // SM sixteen warps; then they are split until it has, or until each row
 // group has one row.
 void plan_rows(RowParams& p, int D) {
-  const int groups = 32 / (D / 8);
+  const int groups = 32 / (D / 16);
   const int64_t want = 148 * 16;
   int64_t n = p.T > 0 ? (want + p.T - 1) / p.T : 1;
   const int hmax = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
@@ -451,7 +483,7 @@ RowParams row_params(const RowsArgs& a) {
   p.slots = a.slots;
   p.n_cache = a.n_cache;
   p.e4m3 = a.e4m3;
-  p.scale[0] = a.k_scale, p.scale[1] = a.v_scale;
+  p.inv_scale[0] = 1.f / a.k_scale, p.inv_scale[1] = 1.f / a.v_scale;
   p.status = a.status;
   return p;
 }
@@ -477,19 +509,28 @@ int launch_rows_bwd_d(const RowsBwdArgs& b) {
   p.dy[0] = b.dq_out, p.dy[1] = b.dk_out;
   p.dxs[0] = b.dq_stride, p.dxs[1] = b.dk_stride;
   p.part = b.part;
-  const int64_t tasks = int64_t(p.T) * p.nslice;
-  int64_t grid = (tasks + kRowWarps - 1) / kRowWarps;
-  if (grid > kRowsBwdMaxBlocks) grid = kRowsBwdMaxBlocks;
+  // two blocks per SM in all, shared between the kinds by their rows
+  int64_t need[2], blocks[2];
+  for (int k = 0; k < 2; ++k)
+    need[k] = (int64_t(p.T) * p.slices[k] + kRowWarps - 1) / kRowWarps;
+  const int64_t H = int64_t(p.H[0]) + p.H[1];
+  for (int k = 0; k < 2; ++k) {
+    const int64_t share = H ? (kRowsBwdMaxBlocks * int64_t(p.H[k]) + H - 1) / H : 0;
+    blocks[k] = need[k] < share ? need[k] : share;
+  }
+  if (blocks[0] + blocks[1] > kRowsBwdMaxBlocks) --blocks[blocks[0] > blocks[1] ? 0 : 1];
+  p.blocks_q = int32_t(blocks[0]);
+  const uint32_t grid = uint32_t(blocks[0] + blocks[1]);
   if (grid > 0) {  // without tokens the weight gradients are zero
     if (b.rows.how.interleaved)
-      rows_bwd_kernel<T, D, true><<<uint32_t(grid), kRowThreads, 0, b.rows.stream>>>(p);
+      rows_bwd_kernel<T, D, true><<<grid, kRowThreads, 0, b.rows.stream>>>(p);
     else
-      rows_bwd_kernel<T, D, false><<<uint32_t(grid), kRowThreads, 0, b.rows.stream>>>(p);
+      rows_bwd_kernel<T, D, false><<<grid, kRowThreads, 0, b.rows.stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   }
   if (!b.dq_weight && !b.dk_weight) return PSA_OK;
-  weight_sum_kernel<<<2 * D / 32, 256, 0, b.rows.stream>>>(b.part, int(grid), D, b.dq_weight,
-                                                           b.dk_weight);
+  weight_sum_kernel<<<dim3(D / 32, 2), 256, 0, b.rows.stream>>>(
+      b.part, p.blocks_q, int(grid), D, b.dq_weight, b.dk_weight);
   return cudaGetLastError() == cudaSuccess ? PSA_OK : PSA_ERR_CUDA;
 }
 
