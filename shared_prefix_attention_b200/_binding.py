@@ -563,15 +563,23 @@ def verify_extend(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr: torch.
 
 # ---------------------------------------------------------------- around a layer's attention
 
+# Short forms of torch.cuda.current_device() and current_stream().cuda_stream:
+# a decoding step's calls take a few microseconds on the GPU, so every
+# microsecond of the host's part counts.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(name: str, device, *args):
     """Calls ``name`` on ``device``'s current stream, with ``device`` current
     (launches and tensor maps belong to the current device's context)."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = getattr(_lib or lib(), name)
+    index = device.index
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, _raw_stream(index))
     if rc != PSA_OK:
         raise PsaError(rc, name)
 
@@ -587,8 +595,7 @@ def _need(ok: bool, what: str):
 
 def _dense(t, shape, dtype, device, name: str):
     """A contiguous CUDA tensor of this shape, dtype and device."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
-            or not t.is_contiguous()):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor {tuple(shape)} on {device} is "
                          f"needed, not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t
@@ -610,26 +617,31 @@ _WEIGHT_DTYPES = {torch.bfloat16: PSA_BF16, torch.float32: PSA_F32}
 
 def _norm_rope(T: int, d: int, device, positions, cos_sin, q_weight, k_weight, eps, interleaved):
     """The psa_norm_rope of these arguments (the tensors are the caller's)."""
-    how = NormRope()
+    pos = cs = qw = kw = None
+    n_pos = rot = wdt = 0
     if cos_sin is not None:
-        _need(positions is not None, "a rotation (cos_sin) needs positions")
-        _dense(positions, (T,), torch.int32, device, "positions")
-        _need(cos_sin.dim() == 2, "cos_sin: [positions, rot_dim] is needed")
-        _dense(cos_sin, cos_sin.shape, torch.float32, device, "cos_sin")
-        how.positions, how.cos_sin = positions.data_ptr(), cos_sin.data_ptr()
-        how.n_positions, how.rot_dim = cos_sin.shape
-        how.interleaved = int(interleaved)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        _need(w.dtype in _WEIGHT_DTYPES, f"{name}: bf16 or fp32 weights are needed")
-        _dense(w, (d,), w.dtype, device, name)
-        setattr(how, name, w.data_ptr())
-        how.weight_dtype = _WEIGHT_DTYPES[w.dtype]
-    _need(q_weight is None or k_weight is None or q_weight.dtype == k_weight.dtype,
-          "q_weight and k_weight have to be of one dtype")
-    how.eps = float(eps)
-    return how
+        if positions is None:
+            raise ValueError("a rotation (cos_sin) needs positions")
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin: [positions, rot_dim] is needed")
+        pos = _dense(positions, (T,), torch.int32, device, "positions").data_ptr()
+        n_pos, rot = cos_sin.shape
+        cs = _dense(cos_sin, (n_pos, rot), torch.float32, device, "cos_sin").data_ptr()
+    if q_weight is not None:
+        wdt = _weight_dtype(q_weight, "q_weight")
+        qw = _dense(q_weight, (d,), q_weight.dtype, device, "q_weight").data_ptr()
+    if k_weight is not None:
+        if q_weight is not None and k_weight.dtype is not q_weight.dtype:
+            raise ValueError("q_weight and k_weight have to be of one dtype")
+        wdt = _weight_dtype(k_weight, "k_weight")
+        kw = _dense(k_weight, (d,), k_weight.dtype, device, "k_weight").data_ptr()
+    return ctypes.byref(NormRope(pos, cs, n_pos, rot, bool(interleaved), qw, kw, wdt, eps))
+
+
+def _weight_dtype(w, name: str) -> int:
+    if w.dtype not in _WEIGHT_DTYPES:
+        raise ValueError(f"{name}: bf16 or fp32 is needed")
+    return _WEIGHT_DTYPES[w.dtype]
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -649,12 +661,12 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     Tk, Hkv, dk, ks = _rows(k, q.dtype, dev, "k")
     _need(Tk == T and dk == d, "q and k have to agree in tokens and head size")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
-    q_out = (torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if q_out is None
+    q_out = (q.new_empty((T, Hq, d)) if q_out is None
              else _dense(q_out, (T, Hq, d), q.dtype, dev, "q_out"))
-    k_out = (torch.empty((T, Hkv, d), dtype=q.dtype, device=dev) if k_out is None
+    k_out = (q.new_empty((T, Hkv, d)) if k_out is None
              else _dense(k_out, (T, Hkv, d), q.dtype, dev, "k_out"))
     _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks,
-            _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, ctypes.byref(how), q_out.data_ptr(),
+            _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how, q_out.data_ptr(),
             k_out.data_ptr(), _addr(status))
     return q_out, k_out
 
@@ -674,18 +686,24 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_
     _dense(dq_out, (T, Hq, d), q.dtype, dev, "dq_out")
     _dense(dk_out, (T, Hkv, d), q.dtype, dev, "dk_out")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
-    dq = torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty((T, Hkv, d), dtype=q.dtype, device=dev) if dk is None else dk
-    _need(tuple(dq.shape) == (T, Hq, d) and tuple(dk.shape) == (T, Hkv, d),
-          "dq and dk have to be shaped as q and k")
-    dqs, dks = _rows(dq, q.dtype, dev, "dq")[3], _rows(dk, q.dtype, dev, "dk")[3]
+    dqs, dks = Hq * d, Hkv * d
+    if dq is None:
+        dq = q.new_empty((T, Hq, d))
+    else:
+        _need(dq.shape == q.shape, "dq has to be shaped as q")
+        dqs = _rows(dq, q.dtype, dev, "dq")[3]
+    if dk is None:
+        dk = q.new_empty((T, Hkv, d))
+    else:
+        _need(dk.shape == k.shape, "dk has to be shaped as k")
+        dks = _rows(dk, q.dtype, dev, "dk")[3]
     dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8,
                                 device=dev)
     _launch("psa_qk_norm_rope_bwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, dq_out.data_ptr(),
-            dk_out.data_ptr(), _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, ctypes.byref(how),
+            dk_out.data_ptr(), _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how,
             dq.data_ptr(), dqs, dk.data_ptr(), dks, _addr(dqw), _addr(dkw), workspace.data_ptr(),
             workspace.numel(), _addr(status))
     return dq, dk, dqw, dkw
@@ -696,17 +714,21 @@ _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 def _caches(k_cache, v_cache, k_scale, v_scale, device):
     """(tokens, heads, d, scales or None) of a pair of cache tensors."""
-    e4m3 = k_scale is not None or v_scale is not None
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(c.dim() == 3 and c.is_contiguous() and c.device == device and c.is_cuda,
-              f"{name}: a contiguous tensor [tokens, Hkv, d] on {device} is needed")
-        _need(c.dtype in _E4M3_DTYPES if e4m3 else c.dtype == torch.bfloat16,
-              f"{name}: bf16, or e4m3 bytes with k_scale and v_scale, is needed")
-    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache have to be shaped alike")
-    _need(not e4m3 or (k_scale is not None and v_scale is not None),
-          "an e4m3 cache needs both k_scale and v_scale")
-    sc = ctypes.byref(KvScales(float(k_scale), float(v_scale))) if e4m3 else None
-    return (*k_cache.shape, sc)
+    sc = None
+    if k_scale is not None or v_scale is not None:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs both k_scale and v_scale")
+        sc = ctypes.byref(KvScales(k_scale, v_scale))
+        ok = k_cache.dtype in _E4M3_DTYPES and v_cache.dtype in _E4M3_DTYPES
+    else:
+        ok = k_cache.dtype is torch.bfloat16 and v_cache.dtype is torch.bfloat16
+    shape = k_cache.shape
+    if (not ok or len(shape) != 3 or v_cache.shape != shape or not k_cache.is_contiguous()
+            or not v_cache.is_contiguous() or not k_cache.is_cuda or k_cache.device != device
+            or v_cache.device != device):
+        raise ValueError(f"k_cache, v_cache: contiguous tensors [tokens, Hkv, d] on {device} are "
+                         "needed, shaped alike, bf16 or (with k_scale and v_scale) e4m3 bytes")
+    return (*shape, sc)
 
 
 def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None, q_weight=None,
@@ -729,12 +751,12 @@ def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None,
     if q is not None:
         Tq, Hq, dq, qs = _rows(q, torch.bfloat16, dev, "q")
         _need(Tq == T and dq == d, "q, k and v have to agree in tokens and head size")
-        q_out = (torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if q_out is None
+        q_out = (q.new_empty((T, Hq, d)) if q_out is None
                  else _dense(q_out, (T, Hq, d), torch.bfloat16, dev, "q_out"))
     _dense(slots, (T,), torch.int32, dev, "slots")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     _launch("psa_cache_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv,
-            d, ctypes.byref(how), k_cache.data_ptr(), v_cache.data_ptr(), ntok, slots.data_ptr(),
+            d, how, k_cache.data_ptr(), v_cache.data_ptr(), ntok, slots.data_ptr(),
             sc, _addr(q_out) if q is not None else None, _addr(status))
     return q_out if q is not None else None
 
@@ -763,6 +785,9 @@ class ChunkPlan:
 
     def __init__(self, info: ChunkInfo, data: torch.Tensor, workspace_bytes: int):
         self.info, self.data, self.workspace_bytes = info, data, workspace_bytes
+        # read once: a ctypes field costs a call's time
+        self._ref = ctypes.byref(info)
+        self._shape = (info.Hq, info.Hkv, info.head_dim, info.n_keys)
 
 
 def build_chunk_plan(qo_lens, kv_lens, Hq: int, Hkv: int, head_dim: int, window: int = 0,
@@ -810,24 +835,26 @@ def chunk(q, k_cache, v_cache, plan: ChunkPlan, scale: float, kv_indices=None,
     positions are the cache's first rows.  logit_cap c > 0: logits become
     c tanh(logit / c)."""
     dev = q.device
-    info = plan.info
-    ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
+    Hq, Hkv, d, n_keys = plan._shape
+    ntok, Hc, dc, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
     T = q.shape[0]
-    _dense(q, (T, info.Hq, info.head_dim), torch.bfloat16, dev, "q")
-    _need((Hkv, d) == (info.Hkv, info.head_dim), "the caches do not fit the plan's heads")
-    _need(plan.data.device == dev, "the plan is on another device")
+    _dense(q, (T, Hq, d), torch.bfloat16, dev, "q")
+    if Hc != Hkv or dc != d:
+        raise ValueError("the caches do not fit the plan's heads")
+    if plan.data.device != dev:
+        raise ValueError("the plan is on another device")
     if kv_indices is not None:
-        _need(kv_indices.dim() == 1 and kv_indices.numel() >= info.n_keys,
-              f"kv_indices: {info.n_keys} entries are needed")
-        _dense(kv_indices, kv_indices.shape, torch.int32, dev, "kv_indices")
+        n = kv_indices.numel()
+        if n < n_keys:
+            raise ValueError(f"kv_indices: {n_keys} entries are needed")
+        _dense(kv_indices, (n,), torch.int32, dev, "kv_indices")
     out = (torch.empty_like(q) if out is None
-           else _dense(out, q.shape, torch.bfloat16, dev, "out"))
-    lse = (torch.empty((T, info.Hq), dtype=torch.float32, device=dev) if lse is None
-           else _dense(lse, (T, info.Hq), torch.float32, dev, "lse"))
+           else _dense(out, (T, Hq, d), torch.bfloat16, dev, "out"))
+    lse = (torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None
+           else _dense(lse, (T, Hq), torch.float32, dev, "lse"))
     if workspace is None:
         workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
     _launch("psa_chunk_fwd", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ntok,
-            _addr(kv_indices), sc, out.data_ptr(), lse.data_ptr(), T, float(scale),
-            float(logit_cap), ctypes.byref(info), plan.data.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _addr(status))
+            _addr(kv_indices), sc, out.data_ptr(), lse.data_ptr(), T, scale, logit_cap, plan._ref,
+            plan.data.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status))
     return out, lse
