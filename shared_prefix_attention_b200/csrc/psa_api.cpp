@@ -568,7 +568,7 @@ extern "C" int psa_qk_norm_rope_fwd(const void* q, int64_t q_stride, const void*
 }
 
 extern "C" size_t psa_qk_norm_rope_bwd_workspace_size(int32_t head_dim) {
-  return head_dim > 0 ? size_t(kRowsBwdMaxBlocks) * head_dim * sizeof(float) : 0;
+  return head_dim > 0 ? size_t(kRowsBlocks) * head_dim * sizeof(float) : 0;
 }
 
 extern "C" int psa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k,

@@ -160,13 +160,13 @@ struct RowsArgs {
 };
 int launch_rows(const RowsArgs& a);
 
-constexpr int kRowsBwdMaxBlocks = 2 * 148;  // two per SM
+constexpr int kRowsBlocks = 2 * 148;  // two per SM
 struct RowsBwdArgs {
   RowsArgs rows;         // q_out / k_out receive dq / dk
   int64_t dq_stride, dk_stride;
   const void* dq_out;    // upstream gradients of the outputs, dense
   const void* dk_out;
-  float* part;           // [kRowsBwdMaxBlocks][D]
+  float* part;           // [kRowsBlocks][D]
   float* dq_weight;      // [D], nullable
   float* dk_weight;
 };

@@ -13,17 +13,27 @@
 //
 // All of it is bound by memory: each input element is read once and each
 // output element written once, with everything in between in fp32 registers
-// and one rounding at the store.  A row is spread over d/16 lanes of two
-// 8-element pieces each.  In the half-split form a lane's pieces are partners
-// of one another (pairs (i, i + rot/2)), in the interleaved form they are
-// neighbours, so a rotation never leaves its lane; the norm's sum is
-// log2(d/16) shuffles.  (One piece per lane, partners exchanged by eight
-// shuffles a row, took two to three times as long.)  A warp keeps one token's
-// cos/sin and weights in registers over the heads of its task and has kUnroll
-// row groups' loads in flight.
+// and one rounding at the store.
+//
+// Loads.  The heads of a token are contiguous, so each warp keeps a ring of
+// kDepth bulk copies (2 KB of rows each) of its own coming, whatever its
+// registers hold: no other warp takes part, so there is nothing to wait for
+// but one's own bytes.  (Loads into registers, the next batch ahead of the one
+// at hand, reached 4.1 TB/s on the large layout's forward: the weights and
+// angles leave too few registers to have more rows on the way.)
+//
+// Layout.  A row is spread over d/16 lanes of two 8-element pieces each.  In
+// the half-split form a lane's pieces are partners of one another (pairs (i,
+// i + rot/2)), in the interleaved form they are neighbours, so a rotation
+// never leaves its lane; the norm's sum is log2(d/16) shuffles.  (One piece
+// per lane, partners exchanged by eight shuffles a row, took twice as long.)
+// A warp keeps one token's cos/sin and weights in registers over the heads of
+// its task.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "psa_device.cuh"
 #include "psa_internal.h"
@@ -33,33 +43,65 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kStageBytes = 2048;  // of a warp's ring
+constexpr int kDepth = 4;          // stages
+constexpr uint32_t kRowSmem = kRowWarps * kDepth * kStageBytes;
 
-// A lane's share of a row as it was loaded: two pieces of 8 elements.
+// Plain (untiled) bulk copy of contiguous global bytes into shared memory;
+// addresses and size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A warp's ring: stages of shared memory and a barrier each.
+struct Ring {
+  uint8_t* base;
+  uint64_t* bar;
+  uint32_t put = 0, got = 0;  // stages filled and emptied so far
+  __device__ __forceinline__ uint8_t* at(uint32_t n) const {
+    return base + (n % kDepth) * kStageBytes;
+  }
+};
+__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint64_t (*bars)[kDepth]) {
+  const int warp = threadIdx.x >> 5;
+  Ring r;
+  r.base = smem + warp * kDepth * kStageBytes;
+  r.bar = bars[warp];
+  if ((threadIdx.x & 31) == 0) {
+    for (int i = 0; i < kDepth; ++i) mbar_init(r.bar + i, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  return r;
+}
+
+// A lane's share of a row as it was loaded: two pieces of 8 elements; get()
+// gives them as eight pairs for the packed fp32 instructions.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
-  static constexpr int kUnroll = 4;  // row groups in flight
   uint4 v[2];
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int a, int b) {
     v[0] = *reinterpret_cast<const uint4*>(row + a);
     v[1] = *reinterpret_cast<const uint4*>(row + b);
   }
-  __device__ __forceinline__ void get(float (&x)[16]) const {
+  __device__ __forceinline__ void get(uint64_t (&x)[8]) const {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
-        x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < 4; ++i)
+        x[4 * j + i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
 };
 template <>
 struct Raw<float> {
-  static constexpr int kUnroll = 2;
   float4 v[4];
   __device__ __forceinline__ void load(const float* row, int a, int b) {
     v[0] = reinterpret_cast<const float4*>(row + a)[0];
@@ -67,45 +109,51 @@ struct Raw<float> {
     v[2] = reinterpret_cast<const float4*>(row + b)[0];
     v[3] = reinterpret_cast<const float4*>(row + b)[1];
   }
-  __device__ __forceinline__ void get(float (&x)[16]) const {
+  __device__ __forceinline__ void get(uint64_t (&x)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      x[4 * j] = v[j].x, x[4 * j + 1] = v[j].y, x[4 * j + 2] = v[j].z, x[4 * j + 3] = v[j].w;
+      x[2 * j] = f2_pack(v[j].x, v[j].y), x[2 * j + 1] = f2_pack(v[j].z, v[j].w);
   }
 };
 
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int a, int b, const float (&x)[16]) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float* y = x + 8 * j;
-    *reinterpret_cast<uint4*>(row + (j ? b : a)) =
-        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                   pack_bf16(y[6], y[7]));
-  }
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return pack_bf16(lo, hi);
 }
-__device__ __forceinline__ void store_row(float* row, int a, int b, const float (&x)[16]) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int a, int b,
+                                          const uint64_t (&x)[8]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    reinterpret_cast<float4*>(row + (j < 2 ? a : b))[j & 1] =
-        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+  for (int j = 0; j < 2; ++j)
+    *reinterpret_cast<uint4*>(row + (j ? b : a)) =
+        make_uint4(bf16_pair(x[4 * j]), bf16_pair(x[4 * j + 1]), bf16_pair(x[4 * j + 2]),
+                   bf16_pair(x[4 * j + 3]));
+}
+__device__ __forceinline__ void store_row(float* row, int a, int b, const uint64_t (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float4 v;
+    f2_unpack(x[2 * j], v.x, v.y);
+    f2_unpack(x[2 * j + 1], v.z, v.w);
+    reinterpret_cast<float4*>(row + (j < 2 ? a : b))[j & 1] = v;
+  }
 }
 // e4m3(x * inv), inv = 1 / scale in fp32 (a step of fp32 from the quotient at
 // most), saturating at +-448 (NaN stays NaN).
-__device__ __forceinline__ void store_row_e4m3(uint8_t* row, int a, int b, const float (&x)[16],
-                                               float inv) {
+__device__ __forceinline__ void store_row_e4m3(uint8_t* row, int a, int b,
+                                               const uint64_t (&x)[8], float inv) {
+  const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    uint32_t w[2];
+    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* y = x + 8 * j + 4 * i;
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      w[i] = lo | (hi << 16);
+    for (int i = 0; i < 4; ++i) {
+      float2 y;
+      f2_unpack(f2_mul(x[4 * j + i], inv2), y.x, y.y);
+      h[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     }
-    *reinterpret_cast<uint2*>(row + (j ? b : a)) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + (j ? b : a)) =
+        make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   }
 }
 
@@ -133,32 +181,55 @@ __device__ __forceinline__ Pieces pieces_of(int l, int rot) {
   return s;
 }
 
-// The lane's eight angles of one position; dir -1 turns back.
-__device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const float* cos_sin,
-                                          int rot, int l, float dir) {
+// A rotation as x' = x k1 + partner(x) k2, element by element: k1 the cosines,
+// k2 the sines with the partner's sign; dir -1 turns back.  Half-split: the
+// partner of pair i (of 8) is pair i ^ 4; interleaved: the pair swapped.
+struct Turn {
+  uint64_t k1[8], k2[8];
+};
+template <bool INTER>
+__device__ __forceinline__ void load_turn(Turn& t, const float* cos_sin, int rot, int l,
+                                          float dir) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(cos_sin + 8 * l + i));
-    const float4 y = __ldg(reinterpret_cast<const float4*>(cos_sin + rot / 2 + 8 * l + i));
-    c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-    s[i] = dir * y.x, s[i + 1] = dir * y.y, s[i + 2] = dir * y.z, s[i + 3] = dir * y.w;
+  for (int i = 0; i < 2; ++i) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cos_sin + 8 * l) + i);
+    float4 s = __ldg(reinterpret_cast<const float4*>(cos_sin + rot / 2 + 8 * l) + i);
+    s.x *= dir, s.y *= dir, s.z *= dir, s.w *= dir;
+    if constexpr (INTER) {
+      t.k1[4 * i] = f2_pack(c.x, c.x), t.k1[4 * i + 1] = f2_pack(c.y, c.y);
+      t.k1[4 * i + 2] = f2_pack(c.z, c.z), t.k1[4 * i + 3] = f2_pack(c.w, c.w);
+      t.k2[4 * i] = f2_pack(-s.x, s.x), t.k2[4 * i + 1] = f2_pack(-s.y, s.y);
+      t.k2[4 * i + 2] = f2_pack(-s.z, s.z), t.k2[4 * i + 3] = f2_pack(-s.w, s.w);
+    } else {
+      t.k1[2 * i] = t.k1[4 + 2 * i] = f2_pack(c.x, c.y);
+      t.k1[2 * i + 1] = t.k1[5 + 2 * i] = f2_pack(c.z, c.w);
+      t.k2[2 * i] = f2_pack(-s.x, -s.y), t.k2[2 * i + 1] = f2_pack(-s.z, -s.w);
+      t.k2[4 + 2 * i] = f2_pack(s.x, s.y), t.k2[5 + 2 * i] = f2_pack(s.z, s.w);
+    }
   }
 }
 template <bool INTER>
-__device__ __forceinline__ void turn_row(const float (&c)[8], const float (&s)[8],
-                                         float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& a = x[INTER ? 2 * i : i];
-    float& b = x[INTER ? 2 * i + 1 : 8 + i];
-    const float a0 = a, b0 = b;
-    a = a0 * c[i] - b0 * s[i];
-    b = a0 * s[i] + b0 * c[i];
+__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[8], int i) {
+  if constexpr (INTER) {
+    float lo, hi;
+    f2_unpack(x[i], lo, hi);
+    return f2_pack(hi, lo);
+  } else {
+    return x[i ^ 4];
   }
+}
+template <bool INTER>
+__device__ __forceinline__ void turn_row(const Turn& t, uint64_t (&x)[8]) {
+  uint64_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    y[i] = f2_fma(partner<INTER>(x, i), t.k2[i], f2_mul(x[i], t.k1[i]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = y[i];
 }
 
 __device__ __forceinline__ void load_weight(const void* w, int dtype, const Pieces& pc,
-                                            float (&x)[16]) {
+                                            uint64_t (&x)[8]) {
   if (dtype == PSA_F32) {
     Raw<float> r;
     r.load(static_cast<const float*>(w), pc.a, pc.b);
@@ -169,6 +240,21 @@ __device__ __forceinline__ void load_weight(const void* w, int dtype, const Piec
     r.get(x);
   }
 }
+__device__ __forceinline__ float pair_sum(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return lo + hi;
+}
+// sum of a[i] b[i] over the lane's 16 elements
+__device__ __forceinline__ float dot16(const uint64_t (&a)[8], const uint64_t (&b)[8]) {
+  uint64_t s0 = f2_mul(a[0], b[0]), s1 = f2_mul(a[1], b[1]);
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) {
+    s0 = f2_fma(a[i], b[i], s0);
+    s1 = f2_fma(a[i + 1], b[i + 1], s1);
+  }
+  return pair_sum(f2_add(s0, s1));
+}
 
 struct RowParams {
   const void *x[3];      // q, k, v rows in
@@ -178,6 +264,7 @@ struct RowParams {
   int32_t slices[3];     // warps a token's heads of the kind are split over
   int32_t hs;            // heads per slice
   int32_t nslice;        // slices[0] + slices[1] + slices[2]
+  bool whole;            // the warps take whole tokens
   int32_t T;
   const int32_t* pos;
   const float* cos_sin;
@@ -209,14 +296,34 @@ __device__ __forceinline__ int64_t token_angle(const RowParams& p, int t, int la
   return at;
 }
 
-// Task -> (token, kind, first head, end head).
+// One task: heads [h0, h1) of one kind of one token.
 struct Task {
   int t, kind, h0, h1;
 };
-__device__ __forceinline__ Task task_of(const RowParams& p, int64_t task) {
+
+// A warp's walk over its tasks.  With tokens enough for every warp (no heads
+// split, see plan_rows) it takes whole tokens, so that the kinds' sizes even
+// out; otherwise single tasks, whose number then fits 32 bits.
+struct Walk {
+  int64_t i;  // token, or task
+  int s = 0;  // slice of the token
+};
+__device__ __forceinline__ bool walk_ends(const RowParams& p, const Walk& w) {
+  return w.i >= (p.whole ? int64_t(p.T) : int64_t(p.T) * p.nslice);
+}
+__device__ __forceinline__ void walk_on(const RowParams& p, Walk& w, int64_t stride) {
+  if (p.whole && ++w.s < p.nslice) return;
+  w.s = 0;
+  w.i += stride;
+}
+__device__ __forceinline__ Task task_at(const RowParams& p, const Walk& w) {
   Task k;
-  k.t = int(task / p.nslice);
-  int s = int(task - int64_t(k.t) * p.nslice);
+  int s = w.s;
+  k.t = int(w.i);
+  if (!p.whole) {
+    k.t = int(uint32_t(w.i) / uint32_t(p.nslice));
+    s = int(uint32_t(w.i) - uint32_t(k.t) * uint32_t(p.nslice));
+  }
   k.kind = 0;
   while (k.kind < 2 && s >= p.slices[k.kind]) s -= p.slices[k.kind++];
   k.h0 = s * p.hs;
@@ -224,151 +331,257 @@ __device__ __forceinline__ Task task_of(const RowParams& p, int64_t task) {
   return k;
 }
 
-// Forward and append: one warp per task, its row groups kUnroll at a time.
+// Forward and append: the warps stride over the tasks.
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
-  constexpr int LPR = D / 16, GROUPS = 32 / LPR, U = Raw<T>::kUnroll;
+__global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
+  constexpr int LPR = D / 16, GROUPS = 32 / LPR;
+  constexpr int ROWS = kStageBytes / (D * int(sizeof(T)));  // rows of a stage
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kRowWarps][kDepth];
+  __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
-  const int64_t task = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (task >= int64_t(p.T) * p.nslice) return;
-  const Task k = task_of(p, task);
-  // where the rows go: dense by token, or the token's cache row
-  int64_t out_row = k.t;
-  if (p.slots && k.kind > 0) {
-    const int32_t slot = __ldg(p.slots + k.t);
-    if (slot < 0) return;  // a padded token: nothing is cached
-    if (slot >= p.n_cache) {
-      if (lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
-      return;
-    }
-    out_row = slot;
-  }
-  const int64_t at = token_angle(p, k.t, lane);
-  if (at < 0) return;
-  const bool norms = k.kind < 2 && p.w[k.kind] != nullptr;
-  const Pieces pc = pieces_of<INTER>(l, k.kind < 2 ? p.rot : 0);
-  float c[8], s[8], w[16];
-  if (pc.on) load_turn(c, s, p.cos_sin + at * p.rot, p.rot, l, 1.f);
-  if (norms) load_weight(p.w[k.kind], p.w_dtype, pc, w);
-  const T* x0 = static_cast<const T*>(p.x[k.kind]) + int64_t(k.t) * p.xs[k.kind];
-  const size_t y0 = size_t(out_row) * p.H[k.kind];
+  if (threadIdx.x == 0) abort_flag = 0;
+  __syncthreads();
+  const int64_t stride = int64_t(gridDim.x) * kRowWarps;
+  Walk walk;
+  walk.i = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  Ring ring = make_ring(smem, bars);
 
-  for (int hb = k.h0; hb < k.h1; hb += GROUPS * U) {
-    Raw<T> raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * GROUPS + g;
-      if (h < k.h1) raw[u].load(x0 + size_t(h) * D, pc.a, pc.b);
+  // the copies run ahead: their own walk over the tasks
+  Walk next = walk;
+  Task n = {};
+  int nh = 0;
+  auto put = [&]() {
+    if (nh >= n.h1) {
+      if (walk_ends(p, next)) return;
+      n = task_at(p, next);
+      nh = n.h0;
+      walk_on(p, next, stride);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * GROUPS + g;
-      if (hb + u * GROUPS >= k.h1) break;  // uniform: every lane takes part in the shuffles
-      float x[16];
-      raw[u].get(x);
+    if (lane == 0) {
+      const T* src = static_cast<const T*>(p.x[n.kind]) + int64_t(n.t) * p.xs[n.kind] +
+                     size_t(nh) * D;
+      const uint32_t bytes = uint32_t(min(ROWS, n.h1 - nh)) * D * sizeof(T);
+      uint64_t* bar = ring.bar + ring.put % kDepth;
+      mbar_arrive_expect_tx(bar, bytes);
+      bulk_load(smem_u32(ring.at(ring.put)), src, bytes, bar);
+    }
+    nh += ROWS;
+    ++ring.put;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) put();
+
+  bool ok = true;
+  for (; ok && !walk_ends(p, walk); walk_on(p, walk, stride)) {
+    const Task k = task_at(p, walk);
+    // where the rows go: dense by token, or the token's cache row (a padded
+    // token caches nothing)
+    int64_t out_row = k.t;
+    bool live = true;
+    if (p.slots && k.kind > 0) {
+      const int32_t slot = __ldg(p.slots + k.t);
+      if (slot >= p.n_cache && lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
+      live = slot >= 0 && slot < p.n_cache;
+      out_row = slot;
+    }
+    const int64_t at = live ? token_angle(p, k.t, lane) : -1;
+    live = at >= 0;
+    const bool norms = k.kind < 2 && p.w[k.kind] != nullptr;
+    const Pieces pc = pieces_of<INTER>(l, k.kind < 2 ? p.rot : 0);
+    // The weights are folded into the rotation: (x w r) k1 + (its partner) k2
+    // = r (x (w k1) + partner(x) (partner(w) k2)); without a rotation k1 = w.
+    Turn turn;
+    uint64_t w[8];
+    if (norms) load_weight(p.w[k.kind], p.w_dtype, pc, w);
+    if (pc.on && live) {
+      load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, 1.f);
       if (norms) {
-        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s0 = fmaf(x[i], x[i], s0);
-          s1 = fmaf(x[8 + i], x[8 + i], s1);
+          turn.k1[i] = f2_mul(turn.k1[i], w[i]);
+          turn.k2[i] = f2_mul(turn.k2[i], partner<INTER>(w, i));
         }
-        const float r = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
       }
-      if (pc.on) turn_row<INTER>(c, s, x);
-      if (h >= k.h1) continue;
-      const size_t off = (y0 + h) * D;
-      if (k.kind > 0 && p.e4m3)
-        store_row_e4m3(static_cast<uint8_t*>(p.y[k.kind]) + off, pc.a, pc.b, x,
-                       p.inv_scale[k.kind - 1]);
-      else
-        store_row(static_cast<T*>(p.y[k.kind]) + off, pc.a, pc.b, x);
+    } else if (norms) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn.k1[i] = w[i];
+    }
+    const size_t y0 = size_t(out_row) * p.H[k.kind];
+
+    for (int hb = k.h0; hb < k.h1; hb += ROWS) {
+      ok = mbar_wait(ring.bar + ring.got % kDepth, (ring.got / kDepth) & 1, &abort_flag, p.status);
+      if (!ok) break;
+      const T* rows = reinterpret_cast<const T*>(ring.at(ring.got));
+#pragma unroll
+      for (int u = 0; u < ROWS / GROUPS; ++u) {
+        const int h = hb + u * GROUPS + g;
+        if (!live || hb + u * GROUPS >= k.h1) break;  // uniform: all lanes shuffle
+        uint64_t x[8];
+        Raw<T> raw;
+        raw.load(rows + (u * GROUPS + g) * D, pc.a, pc.b);
+        raw.get(x);
+        float r = 1.f;
+        if (norms) r = rsqrtf(row_sum<LPR>(dot16(x, x)) * (1.f / D) + p.eps);
+        if (pc.on) {
+          turn_row<INTER>(turn, x);
+        } else if (norms) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = f2_mul(x[i], turn.k1[i]);
+        }
+        if (norms) {
+          const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = f2_mul(x[i], r2);
+        }
+        if (h < k.h1) {
+          const size_t off = (y0 + h) * D;
+          if (k.kind > 0 && p.e4m3)
+            store_row_e4m3(static_cast<uint8_t*>(p.y[k.kind]) + off, pc.a, pc.b, x,
+                           p.inv_scale[k.kind - 1]);
+          else
+            store_row(static_cast<T*>(p.y[k.kind]) + off, pc.a, pc.b, x);
+        }
+      }
+      ++ring.got;
+      __syncwarp();  // every lane has read the stage
+      put();
+    }
+  }
+  if (!ok && lane == 0) {
+    // let copies in flight land before the block exits
+    const uint64_t w0 = globaltimer();
+    while (globaltimer() - w0 < 1000000ull) {
     }
   }
 }
 
 // Backward: every block works on one kind and strides over its tasks, so that
 // it sums its rows' weight gradients in registers and writes one partial; the
-// order of every sum is fixed by the sizes alone.
+// order of every sum is fixed by the sizes alone.  A stage holds rows of x and
+// of the upstream gradient.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
-  constexpr int LPR = D / 16, GROUPS = 32 / LPR, U = Raw<T>::kUnroll / 2;
+  constexpr int LPR = D / 16, GROUPS = 32 / LPR;
+  constexpr int HALF = kStageBytes / 2;
+  // at least one row group; fp32 rows of 16 lanes fill the stage with less
+  constexpr int ROWS = HALF / (D * int(sizeof(T)));
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[kRowWarps][D];
+  __shared__ uint64_t bars[kRowWarps][kDepth];
+  __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, g = lane / LPR;
+  if (threadIdx.x == 0) abort_flag = 0;
+  __syncthreads();
   const int kind = int(blockIdx.x) < p.blocks_q ? 0 : 1;
   const int block = int(blockIdx.x) - (kind ? p.blocks_q : 0);
   const int blocks = kind ? int(gridDim.x) - p.blocks_q : p.blocks_q;
   const Pieces pc = pieces_of<INTER>(l, p.rot);
   const bool norms = p.w[kind] != nullptr;
   const int H = p.H[kind], slices = p.slices[kind];
-  float w[16], dw[16];
+  uint64_t w[8], dw[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[i] = 0ull;
   if (norms) load_weight(p.w[kind], p.w_dtype, pc, w);
   const int64_t tasks = int64_t(p.T) * slices;
-  for (int64_t task = int64_t(block) * kRowWarps + warp; task < tasks;
-       task += int64_t(blocks) * kRowWarps) {
-    const int t = int(task / slices);
+  const int64_t stride = int64_t(blocks) * kRowWarps;
+  int64_t task = int64_t(block) * kRowWarps + warp;
+  Ring ring = make_ring(smem, bars);
+
+  // (heads are only split where the tasks fit 32 bits, see plan_rows)
+  auto token_of = [&](int64_t i) {
+    return slices == 1 ? int(i) : int(uint32_t(i) / uint32_t(slices));
+  };
+  int64_t next = task;
+  int nt = 0, nh = 0, nh1 = 0;
+  auto put = [&]() {
+    if (nh >= nh1) {
+      if (next >= tasks) return;
+      nt = token_of(next);
+      nh = int(next - int64_t(nt) * slices) * p.hs;
+      nh1 = min(nh + p.hs, H);
+      next += stride;
+    }
+    if (lane == 0) {
+      const uint32_t bytes = uint32_t(min(ROWS, nh1 - nh)) * D * sizeof(T);
+      uint64_t* bar = ring.bar + ring.put % kDepth;
+      const uint32_t dst = smem_u32(ring.at(ring.put));
+      mbar_arrive_expect_tx(bar, norms ? 2 * bytes : bytes);
+      bulk_load(dst, static_cast<const T*>(p.dy[kind]) + (int64_t(nt) * H + nh) * D, bytes, bar);
+      if (norms)
+        bulk_load(dst + HALF, static_cast<const T*>(p.x[kind]) + int64_t(nt) * p.xs[kind] +
+                                  size_t(nh) * D, bytes, bar);
+    }
+    nh += ROWS;
+    ++ring.put;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) put();
+
+  bool ok = true;
+  for (; task < tasks && ok; task += stride) {
+    const int t = token_of(task);
     const int h0 = int(task - int64_t(t) * slices) * p.hs, h1 = min(h0 + p.hs, H);
     const int64_t at = token_angle(p, t, lane);
-    if (at < 0) continue;
-    float c[8], s[8];
-    if (pc.on) load_turn(c, s, p.cos_sin + at * p.rot, p.rot, l, -1.f);
-    const T* x0 = static_cast<const T*>(p.x[kind]) + int64_t(t) * p.xs[kind];
-    const T* g0 = static_cast<const T*>(p.dy[kind]) + int64_t(t) * H * D;
+    const bool live = at >= 0;
+    Turn turn;
+    if (pc.on && live) load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, -1.f);
     T* d0 = static_cast<T*>(p.y[kind]) + int64_t(t) * p.dxs[kind];
-    for (int hb = h0; hb < h1; hb += GROUPS * U) {
-      Raw<T> xr[U], gr[U];
+    for (int hb = h0; hb < h1; hb += ROWS) {
+      ok = mbar_wait(ring.bar + ring.got % kDepth, (ring.got / kDepth) & 1, &abort_flag, p.status);
+      if (!ok) break;
+      const T* gr = reinterpret_cast<const T*>(ring.at(ring.got));
+      const T* xr = reinterpret_cast<const T*>(ring.at(ring.got) + HALF);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * GROUPS + g;
+      for (int u = 0; u < (ROWS + GROUPS - 1) / GROUPS; ++u) {
+        const int i0 = u * GROUPS + g, h = hb + i0;
+        if (!live || hb + u * GROUPS >= h1) break;  // uniform: all lanes shuffle
         // rows behind the last one: zeros, they add nothing to the sums
-        xr[u] = Raw<T>{};
-        gr[u] = Raw<T>{};
-        if (h < h1) {
-          gr[u].load(g0 + size_t(h) * D, pc.a, pc.b);
-          if (norms) xr[u].load(x0 + size_t(h) * D, pc.a, pc.b);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * GROUPS + g;
-        if (hb + u * GROUPS >= h1) break;
-        float dy[16];
-        gr[u].get(dy);
-        if (pc.on) turn_row<INTER>(c, s, dy);
+        const bool row = i0 < ROWS && h < h1;
+        uint64_t dy[8];
+        Raw<T> raw = {};
+        if (row) raw.load(gr + i0 * D, pc.a, pc.b);
+        raw.get(dy);
+        if (pc.on) turn_row<INTER>(turn, dy);
         if (norms) {
-          float x[16];
-          xr[u].get(x);
-          float ss = 0.f, dot = 0.f;
+          uint64_t x[8];
+          raw = Raw<T>{};
+          if (row) raw.load(xr + i0 * D, pc.a, pc.b);
+          raw.get(x);
+          const float r = rsqrtf(row_sum<LPR>(dot16(x, x)) * (1.f / D) + p.eps);
+          const uint64_t r2 = f2_pack(r, r);
+          uint64_t wg[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            ss = fmaf(x[i], x[i], ss);
-            dot = fmaf(w[i] * dy[i], x[i], dot);
+          for (int i = 0; i < 8; ++i) {
+            wg[i] = f2_mul(w[i], dy[i]);
+            dw[i] = f2_fma(f2_mul(dy[i], x[i]), r2, dw[i]);
           }
-          ss = row_sum<LPR>(ss);
-          dot = row_sum<LPR>(dot);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
-          const float e = r * r * dot * (1.f / D);
+          const float e = -r * r * row_sum<LPR>(dot16(wg, x)) * (1.f / D);
+          const uint64_t e2 = f2_pack(e, e);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            dw[i] = fmaf(dy[i], x[i] * r, dw[i]);
-            dy[i] = r * (w[i] * dy[i] - x[i] * e);
-          }
+          for (int i = 0; i < 8; ++i) dy[i] = f2_mul(r2, f2_fma(x[i], e2, wg[i]));
         }
-        if (h < h1) store_row(d0 + size_t(h) * D, pc.a, pc.b, dy);
+        if (row) store_row(d0 + size_t(h) * D, pc.a, pc.b, dy);
       }
+      ++ring.got;
+      __syncwarp();  // every lane has read the stage
+      put();
+    }
+  }
+  if (!ok && lane == 0) {
+    // let copies in flight land before the block exits
+    const uint64_t w0 = globaltimer();
+    while (globaltimer() - w0 < 1000000ull) {
     }
   }
   // the row groups of a warp, then the warps of the block
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float v = dw[i];
+  for (int i = 0; i < 8; ++i) {
+    uint64_t v = dw[i];
 #pragma unroll
-    for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (g == 0) red[warp][(i < 8 ? pc.a : pc.b) + (i & 7)] = v;
+    for (int off = LPR; off < 32; off <<= 1) v = f2_add(v, __shfl_xor_sync(0xffffffffu, v, off));
+    float* at = red[warp] + (i < 4 ? pc.a : pc.b) + 2 * (i & 3);
+    if (g == 0) f2_unpack(v, at[0], at[1]);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += kRowThreads) {
@@ -446,19 +659,19 @@ __global__ void __launch_bounds__(256) cache_read_kernel(
   }
 }
 
-// Heads per warp: a token's heads of a kind stay in one warp (its angles and
-// weights are loaded once) unless the call has too few tokens to give every
-// SM sixteen warps; then they are split until it has, or until each row
-// group has one row.
+// Heads per task: all of a token's heads of a kind (its angles and weights are
+// loaded once) unless the call has too few tokens to give every SM sixteen
+// warps; then they are split until it has, or until a task is one row group.
 void plan_rows(RowParams& p, int D) {
   const int groups = 32 / (D / 16);
-  const int64_t want = 148 * 16;
-  int64_t n = p.T > 0 ? (want + p.T - 1) / p.T : 1;
+  const int64_t want = kRowsBlocks * kRowWarps;
+  const int64_t n = p.T > 0 ? (want + p.T - 1) / p.T : 1;
   const int hmax = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
   int64_t hs = (hmax + n - 1) / n;
   hs = (hs + groups - 1) / groups * groups;
   if (hs < groups) hs = groups;
   p.hs = int32_t(hs);
+  p.whole = n == 1;
   p.nslice = 0;
   for (int k = 0; k < 3; ++k) {
     p.slices[k] = (p.H[k] + p.hs - 1) / p.hs;
@@ -488,18 +701,31 @@ RowParams row_params(const RowsArgs& a) {
   return p;
 }
 
+// Launches with the ring's shared memory (opted in once per device).
+template <void (*KERNEL)(RowParams)>
+int launch_ring(uint32_t grid, cudaStream_t stream, const RowParams& p) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PSA_ERR_CUDA;
+  if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kRowSmem)) != cudaSuccess)
+      return PSA_ERR_CUDA;
+    if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
+  KERNEL<<<grid, kRowThreads, kRowSmem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PSA_OK : PSA_ERR_CUDA;
+}
+
 template <typename T, int D>
 int launch_rows_d(const RowsArgs& a) {
   RowParams p = row_params(a);
   plan_rows(p, D);
   const int64_t tasks = int64_t(p.T) * p.nslice;
-  const int64_t grid = (tasks + kRowWarps - 1) / kRowWarps;
-  if (grid > INT32_MAX) return PSA_ERR_INVALID_ARG;
-  if (a.how.interleaved)
-    rows_kernel<T, D, true><<<uint32_t(grid), kRowThreads, 0, a.stream>>>(p);
-  else
-    rows_kernel<T, D, false><<<uint32_t(grid), kRowThreads, 0, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PSA_OK : PSA_ERR_CUDA;
+  int64_t grid = ((p.whole ? int64_t(p.T) : tasks) + kRowWarps - 1) / kRowWarps;
+  if (grid > kRowsBlocks) grid = kRowsBlocks;
+  return a.how.interleaved ? launch_ring<rows_kernel<T, D, true>>(uint32_t(grid), a.stream, p)
+                           : launch_ring<rows_kernel<T, D, false>>(uint32_t(grid), a.stream, p);
 }
 
 template <typename T, int D>
@@ -515,18 +741,17 @@ int launch_rows_bwd_d(const RowsBwdArgs& b) {
     need[k] = (int64_t(p.T) * p.slices[k] + kRowWarps - 1) / kRowWarps;
   const int64_t H = int64_t(p.H[0]) + p.H[1];
   for (int k = 0; k < 2; ++k) {
-    const int64_t share = H ? (kRowsBwdMaxBlocks * int64_t(p.H[k]) + H - 1) / H : 0;
+    const int64_t share = H ? (kRowsBlocks * int64_t(p.H[k]) + H - 1) / H : 0;
     blocks[k] = need[k] < share ? need[k] : share;
   }
-  if (blocks[0] + blocks[1] > kRowsBwdMaxBlocks) --blocks[blocks[0] > blocks[1] ? 0 : 1];
+  if (blocks[0] + blocks[1] > kRowsBlocks) --blocks[blocks[0] > blocks[1] ? 0 : 1];
   p.blocks_q = int32_t(blocks[0]);
   const uint32_t grid = uint32_t(blocks[0] + blocks[1]);
   if (grid > 0) {  // without tokens the weight gradients are zero
-    if (b.rows.how.interleaved)
-      rows_bwd_kernel<T, D, true><<<grid, kRowThreads, 0, b.rows.stream>>>(p);
-    else
-      rows_bwd_kernel<T, D, false><<<grid, kRowThreads, 0, b.rows.stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
+    const int rc = b.rows.how.interleaved
+                       ? launch_ring<rows_bwd_kernel<T, D, true>>(grid, b.rows.stream, p)
+                       : launch_ring<rows_bwd_kernel<T, D, false>>(grid, b.rows.stream, p);
+    if (rc != PSA_OK) return rc;
   }
   if (!b.dq_weight && !b.dk_weight) return PSA_OK;
   weight_sum_kernel<<<dim3(D / 32, 2), 256, 0, b.rows.stream>>>(
