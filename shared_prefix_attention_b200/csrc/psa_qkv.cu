@@ -285,15 +285,22 @@ struct RowParams {
   int32_t blocks_q;      // the blocks below it work on q, the others on k
 };
 
-// The token's row in the angle table; -1 (and a report) if it is outside.
-__device__ __forceinline__ int64_t token_angle(const RowParams& p, int t, int lane) {
-  if (p.rot == 0) return 0;
-  const int32_t at = __ldg(p.pos + t);
-  if (at < 0 || at >= p.n_pos) {
-    if (lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
-    return -1;
-  }
-  return at;
+// What a token's rows need besides themselves: its position and cache row,
+// read one task ahead so that a task does not start with their latency.
+struct Place {
+  int32_t at = 0, slot = 0;
+};
+__device__ __forceinline__ Place load_place(const RowParams& p, int t) {
+  Place v;
+  if (p.rot) v.at = __ldg(p.pos + t);
+  if (p.slots) v.slot = __ldg(p.slots + t);
+  return v;
+}
+// Whether the position lies in the angle table (reported if not).
+__device__ __forceinline__ bool place_turns(const RowParams& p, const Place& v, int lane) {
+  if (p.rot == 0 || (v.at >= 0 && v.at < p.n_pos)) return true;
+  if (lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
+  return false;
 }
 
 // One task: heads [h0, h1) of one kind of one token.
@@ -373,20 +380,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   for (int i = 0; i < kDepth; ++i) put();
 
   bool ok = true;
-  for (; ok && !walk_ends(p, walk); walk_on(p, walk, stride)) {
+  Place place = {};
+  if (!walk_ends(p, walk)) place = load_place(p, task_at(p, walk).t);
+  while (ok && !walk_ends(p, walk)) {
     const Task k = task_at(p, walk);
+    const Place here = place;
+    walk_on(p, walk, stride);
+    if (!walk_ends(p, walk)) place = load_place(p, task_at(p, walk).t);
     // where the rows go: dense by token, or the token's cache row (a padded
     // token caches nothing)
     int64_t out_row = k.t;
     bool live = true;
     if (p.slots && k.kind > 0) {
-      const int32_t slot = __ldg(p.slots + k.t);
-      if (slot >= p.n_cache && lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
-      live = slot >= 0 && slot < p.n_cache;
-      out_row = slot;
+      if (here.slot >= p.n_cache && lane == 0) report_status(p.status, PSA_ERR_INVALID_ARG);
+      live = here.slot >= 0 && here.slot < p.n_cache;
+      out_row = here.slot;
     }
-    const int64_t at = live ? token_angle(p, k.t, lane) : -1;
-    live = at >= 0;
+    live = live && place_turns(p, here, lane);
     const bool norms = k.kind < 2 && p.w[k.kind] != nullptr;
     const Pieces pc = pieces_of<INTER>(l, k.kind < 2 ? p.rot : 0);
     // The weights are folded into the rotation: (x w r) k1 + (its partner) k2
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
     uint64_t w[8];
     if (norms) load_weight(p.w[k.kind], p.w_dtype, pc, w);
     if (pc.on && live) {
-      load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, 1.f);
+      load_turn<INTER>(turn, p.cos_sin + int64_t(here.at) * p.rot, p.rot, l, 1.f);
       if (norms) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -519,13 +529,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
   for (int i = 0; i < kDepth; ++i) put();
 
   bool ok = true;
+  Place place = {};
+  if (task < tasks) place = load_place(p, token_of(task));
   for (; task < tasks && ok; task += stride) {
     const int t = token_of(task);
     const int h0 = int(task - int64_t(t) * slices) * p.hs, h1 = min(h0 + p.hs, H);
-    const int64_t at = token_angle(p, t, lane);
-    const bool live = at >= 0;
+    const Place here = place;
+    if (task + stride < tasks) place = load_place(p, token_of(task + stride));
+    const bool live = place_turns(p, here, lane);
     Turn turn;
-    if (pc.on && live) load_turn<INTER>(turn, p.cos_sin + at * p.rot, p.rot, l, -1.f);
+    if (pc.on && live)
+      load_turn<INTER>(turn, p.cos_sin + int64_t(here.at) * p.rot, p.rot, l, -1.f);
     T* d0 = static_cast<T*>(p.y[kind]) + int64_t(t) * p.dxs[kind];
     for (int hb = h0; hb < h1; hb += ROWS) {
       ok = mbar_wait(ring.bar + ring.got % kDepth, (ring.got / kDepth) & 1, &abort_flag, p.status);
