@@ -100,6 +100,7 @@ struct Params {
   const int32_t* kv_indices;
   int64_t n_keys;
   __nv_bfloat16* o;
+  bool o_wide;  // o is 32-byte aligned
   float* lse;
   int32_t n_rows, Hq, Hkv, G, TPH, window;
   float scale_log2;  // logits in the log2 domain; capped: 2 log2e scale / cap
@@ -192,6 +193,13 @@ __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
     return pack_bf16(lo, hi);
   }
 }
+// 32 bytes in one store: half the store instructions of 16-byte ones (a warp's
+// store touches 32 rows).
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -199,9 +207,10 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // Logits outside [lo, hi) become -inf (their weights exactly 0).
-__device__ __forceinline__ void mask_row(uint32_t (&s)[BN], int lo, int hi) {
+template <int N>
+__device__ __forceinline__ void mask_row(uint32_t (&s)[N], int lo, int hi) {
 #pragma unroll
-  for (int w = 0; w < BN / 32; ++w) {
+  for (int w = 0; w < N / 32; ++w) {
     const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
     const uint32_t below_b = b == 32 ? 0xffffffffu : ((1u << b) - 1u);
     const uint32_t below_a = a == 32 ? 0xffffffffu : ((1u << a) - 1u);
@@ -213,21 +222,21 @@ __device__ __forceinline__ void mask_row(uint32_t (&s)[BN], int lo, int hi) {
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-__device__ __forceinline__ float max_of_row(const uint32_t (&s)[BN]) {
+template <int N>
+__device__ __forceinline__ float max_of_row(const uint32_t (&s)[N]) {
   float v[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(s[k]);
 #pragma unroll
-  for (int k = 8; k < BN - 8; k += 16)
+  for (int k = 8; k < N - 8; k += 16)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v[i] = max3(v[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + 8 + i]));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = max3(v[i], v[i + 4], __uint_as_float(s[BN - 8 + i]));
-  v[0] = max3(v[0], v[1], __uint_as_float(s[BN - 4]));
-  v[2] = max3(v[2], v[3], __uint_as_float(s[BN - 3]));
-  return max3(max3(v[0], v[2], __uint_as_float(s[BN - 2])), v[0],
-                  __uint_as_float(s[BN - 1]));
+  for (int i = 0; i < 4; ++i) v[i] = max3(v[i], v[i + 4], __uint_as_float(s[N - 8 + i]));
+  v[0] = max3(v[0], v[1], __uint_as_float(s[N - 4]));
+  v[2] = max3(v[2], v[3], __uint_as_float(s[N - 3]));
+  return fmaxf(max3(v[0], v[2], __uint_as_float(s[N - 2])), __uint_as_float(s[N - 1]));
 }
 
 // kind::f16 with f16 or bf16 operands and fp32 accumulation.
@@ -252,27 +261,16 @@ __device__ __forceinline__ float to_log2(float s, const Params& p) {
 // Weights of a row of logits against the max -neg_m, packed in pairs into the
 // row's first half (pair k over logit k <= 2 k, which is done by then);
 // returns their fp32 sum.
-template <bool F16, bool CAP>
+template <bool F16>
 __device__ __forceinline__ float weights_row(uint32_t (&s)[BN], float neg_m, const Params& p) {
-  const float cap2 = -2.f * p.cap_log2, top = neg_m + p.cap_log2;
   const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
   for (int k = 0; k < BN / 2; ++k) {
-    const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
-    float p0, p1;
-    if constexpr (CAP) {
-      const float r0 = fast_rcp(1.f + fast_exp2(s0 * p.scale_log2));
-      const float r1 = fast_rcp(1.f + fast_exp2(s1 * p.scale_log2));
-      p0 = s0 == -INFINITY ? 0.f : fast_exp2(fmaf(r0, cap2, top));
-      p1 = s1 == -INFINITY ? 0.f : fast_exp2(fmaf(r1, cap2, top));
-    } else {
-      const uint64_t x2 = f2_fma(f2_pack(s0, s1), sc2, nm2);
-      float x0, x1;
-      f2_unpack(x2, x0, x1);
-      p0 = fast_exp2(x0);
-      p1 = fast_exp2(x1);
-    }
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2, nm2),
+              x0, x1);
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
     acc[k & 3] = f2_add(acc[k & 3], f2_pack(p0, p1));
     s[k] = pack_p<F16>(p0, p1);
   }
@@ -280,6 +278,60 @@ __device__ __forceinline__ float weights_row(uint32_t (&s)[BN], float neg_m, con
 #pragma unroll
   for (int k = 0; k < 4; ++k) f2_unpack(acc[k], v[2 * k], v[2 * k + 1]);
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+// The same of capped logits.  With e = exp(2 s / c) a weight is 2^(c' - m - 2
+// c' / (1 + e)), c' = c log2(e): two exponentials and a reciprocal, which would
+// leave the special-function unit a third of the uncapped rate.  So four
+// reciprocals come from that of the four's product (e is held below 2^30,
+// where the cap is reached to 1e-9, so the product stays finite).  A further
+// step, a part of the first exponentials by a polynomial on the FMA pipe,
+// gained 2 %: the issue slots are then as full as the unit.
+template <bool F16, bool MASKED, int N>
+__device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_m,
+                                                    const Params& p) {
+  const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), one = f2_pack(1.f, 1.f);
+  const uint64_t cap2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
+  const uint64_t top = f2_pack(neg_m + p.cap_log2, neg_m + p.cap_log2);
+  uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k) {
+    uint64_t e[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float x0, x1;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * k + 2 * j]),
+                               __uint_as_float(s[4 * k + 2 * j + 1])), sc2), x0, x1);
+      x0 = fminf(x0, 30.f), x1 = fminf(x1, 30.f);
+      e[j] = f2_pack(fast_exp2(x0), fast_exp2(x1));
+    }
+    const uint64_t ab = f2_add(e[0], one), cd = f2_add(e[1], one);  // (a, b), (c, d)
+    const uint64_t ac_bd = f2_mul(ab, cd);                          // (a c, b d)
+    float ac, bd;
+    f2_unpack(ac_bd, ac, bd);
+    const float r = fast_rcp(ac * bd);
+    const uint64_t rr = f2_mul(f2_pack(r, r), f2_pack(bd, ac));     // 1 / (a c), 1 / (b d)
+    const uint64_t y[2] = {f2_fma(f2_mul(rr, cd), cap2, top), f2_fma(f2_mul(rr, ab), cap2, top)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float x0, x1;
+      f2_unpack(y[j], x0, x1);
+      float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+      if (MASKED) {
+        p0 = s[4 * k + 2 * j] == 0xff800000u ? 0.f : p0;
+        p1 = s[4 * k + 2 * j + 1] == 0xff800000u ? 0.f : p1;
+      }
+      acc[j] = f2_add(acc[j], f2_pack(p0, p1));
+      // packed behind the four's last use of its logits
+      e[j] = pack_p<F16>(p0, p1);
+    }
+    s[2 * k] = uint32_t(e[0]);
+    s[2 * k + 1] = uint32_t(e[1]);
+  }
+  float v[4];
+  f2_unpack(acc[0], v[0], v[1]);
+  f2_unpack(acc[1], v[2], v[3]);
+  return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
 template <int D, bool E4M3, bool CAP>
@@ -715,24 +767,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lo = p.window ? max(pos - p.window + 1 - t, 0) : 0;
         const int hi = min(pos + 1, w.t1) - t;
 
-        // the whole S row in one TMEM load
-        uint32_t sr[BN];
-        tmem_ld128(tS, sr);
-        tmem_wait_ld();
-        if (masked) mask_row(sr, lo, hi);
         // lazy rescaling: the max is raised when it grew by more than 2^8.  O
         // (the PVs of earlier tiles) is rescaled after P is stored, when the S
         // row no longer occupies registers; it only has to happen before this
         // tile's PV, which waits for p_full.
-        const float m_tile = to_log2<CAP>(max_of_row(sr), p);
         float alpha = 1.f;
-        if (m_tile > m_run + kRescaleLog2) {
-          alpha = fast_exp2(m_run - m_tile);
-          l_run *= alpha;
-          m_run = m_tile;
+        auto raise = [&](float m_tile) {
+          if (m_tile > m_run + kRescaleLog2) {
+            alpha = fast_exp2(m_run - m_tile);
+            l_run *= alpha;
+            m_run = m_tile;
+          }
+          return m_run == -INFINITY ? 0.f : -m_run;
+        };
+        if constexpr (CAP) {
+          // half a row at a time, read twice: a capped weight needs more
+          // registers than a whole row leaves
+          uint32_t sr[BN / 2];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld64(tS + c * (BN / 2), sr);
+            tmem_wait_ld();
+            if (masked) mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+            mx = fmaxf(mx, max_of_row(sr));
+          }
+          const float neg_m = raise(to_log2<CAP>(mx, p));
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld64(tS + c * (BN / 2), sr);
+            tmem_wait_ld();
+            if (masked) {
+              mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+              l_run += weights_row_capped<E4M3, true>(sr, neg_m, p);
+            } else {
+              l_run += weights_row_capped<E4M3, false>(sr, neg_m, p);
+            }
+            tmem_st32(tS + c * (BN / 4), *reinterpret_cast<uint32_t(*)[BN / 4]>(sr));
+          }
+        } else {
+          // the whole S row in one TMEM load
+          uint32_t sr[BN];
+          tmem_ld128(tS, sr);
+          tmem_wait_ld();
+          if (masked) mask_row(sr, lo, hi);
+          const float neg_m = raise(to_log2<CAP>(max_of_row(sr), p));
+          l_run += weights_row<E4M3>(sr, neg_m, p);
+          tmem_st64(tS, *reinterpret_cast<uint32_t(*)[BN / 2]>(sr));
         }
-        l_run += weights_row<E4M3, CAP>(sr, m_run == -INFINITY ? 0.f : -m_run, p);
-        tmem_st64(tS, *reinterpret_cast<uint32_t(*)[BN / 2]>(sr));
         if (nt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // wait for the latest PV into O, then scale O by alpha in place
           if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) {
@@ -759,11 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // partial row of this thread's row in the block
-      const size_t prow = size_t(w.part) + (w.twin ? x * w.ntok * p.G : x * p.TPH * p.G) + r;
+      // this thread's row among the block's, and its partial
+      const int brow = (w.twin ? 0 : x * p.TPH * p.G) + r, rows = w.ntok * p.G;
+      const size_t part = size_t(w.part) + (w.twin ? x * rows : 0);
       if (nt == 0) {
         // no tile of this piece is this half's: an empty partial
-        if (valid && w.part >= 0) p.part_lse[prow] = -INFINITY;
+        if (valid && w.part >= 0) p.part_lse[part + brow] = -INFINITY;
         continue;
       }
       // ---- epilogue: O / l straight from TMEM, LSE
@@ -778,26 +861,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tO + c * 32, orr);
         tmem_wait_ld();
         if (valid && w.part >= 0) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+          // partials are laid out [D / 4][rows][4]: the rows of a warp store
+          // next to each other (row-major, 32 rows apart, a unit's epilogue
+          // took 24000 cycles)
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D) + size_t(c) * 8 * rows + brow;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(
+            dst[size_t(k) * rows] = make_float4(
                 __uint_as_float(orr[4 * k]) * inv, __uint_as_float(orr[4 * k + 1]) * inv,
                 __uint_as_float(orr[4 * k + 2]) * inv, __uint_as_float(orr[4 * k + 3]) * inv);
         } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c * 32);
+          uint32_t o[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t o4[4];
+          for (int i = 0; i < 16; ++i)
+            o[i] = pack_bf16(__uint_as_float(orr[2 * i]) * inv,
+                             __uint_as_float(orr[2 * i + 1]) * inv);
+          __nv_bfloat16* dst = p.o + row * D + c * 32;
+          if (p.o_wide) {
+            store32(dst, o);
+            store32(dst + 16, o + 8);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o4[i] = pack_bf16(__uint_as_float(orr[8 * k + 2 * i]) * inv,
-                                __uint_as_float(orr[8 * k + 2 * i + 1]) * inv);
-            dst[k] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<uint4*>(dst)[k] =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
       }
-      if (valid && w.part >= 0) p.part_lse[prow] = lse2;
+      if (valid && w.part >= 0) p.part_lse[part + brow] = lse2;
       if (valid && w.part < 0 && p.lse) p.lse[row] = lse2 * kLn2;
       tc_fence_before();
       __syncwarp();
@@ -812,10 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partials of split blocks by their log2-sum-exp, one warp per row.
+// Joins the partials of split blocks by their log2-sum-exp.  A block of
+// threads has 32 rows, one per lane (as the partials lie); its warps share the
+// columns, and the rows go out through shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
-  constexpr int E = D / 32;
+  constexpr int N = D / 32;  // groups of four columns of a warp: warp, warp + 8, ...
+  constexpr int PITCH = D * 2 + 16;
+  __shared__ __align__(16) uint8_t out[32 * PITCH];
   const ChunkPlanView view(p.n_ctas, p.n_units, p.n_joins);
   if (__ldg(p.plan) != kChunkMagic || __ldg(p.plan + 1) != p.n_ctas ||
       __ldg(p.plan + 2) != p.n_units || __ldg(p.plan + 3) != p.n_joins)
@@ -824,50 +919,58 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
   const int4 a = __ldg(join);
   const int count = __ldg(reinterpret_cast<const int32_t*>(join + 1));
   const int q0 = a.x, rows = a.y, kvh = a.z;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = blockIdx.y * 32;
+  if (row0 >= rows) return;
   if (!psa_in_bounds(q0 >= 0 && rows > 0 && kvh >= 0 && kvh < p.Hkv && a.w >= 0 && count > 0 &&
                          int64_t(q0) + (rows - 1) / p.G < p.n_rows &&
                          a.w + int64_t(count) * rows <= p.part_rows,
-                     lane == 0 ? p.status : nullptr))
+                     threadIdx.x == 0 ? p.status : nullptr))
     return;
+  const int r = min(row0 + lane, rows - 1);
   const float* lse = p.part_lse + a.w + r;
   float m = -INFINITY;
-  for (int i = lane; i < count; i += 32) m = fmaxf(m, lse[size_t(i) * rows]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float acc[E], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const float* o0 = p.part_o + (size_t(a.w) + r) * D + lane * E;
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    const int n = min(32, count - i0);
-    float wl = 0.f;
-    if (lane < n && m != -INFINITY) wl = fast_exp2(lse[size_t(i0 + lane) * rows] - m);
-    sum += wl;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(0xffffffffu, wl, i);
-      if (w == 0.f) continue;  // an empty partial's rows were not written
-      const float* src = o0 + size_t(i0 + i) * rows * D;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-      }
+  for (int i = 0; i < count; ++i) m = fmaxf(m, __ldg(lse + size_t(i) * rows));
+  float4 acc[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const float4* o0 =
+      reinterpret_cast<const float4*>(p.part_o + size_t(a.w) * D) + size_t(warp) * rows + r;
+#pragma unroll 2
+  for (int i = 0; i < count; ++i) {
+    const float l = __ldg(lse + size_t(i) * rows);
+    // an empty partial's rows were not written
+    if (l == -INFINITY) continue;
+    const float w = fast_exp2(l - m);
+    sum += w;
+    const float4* src = o0 + size_t(i) * rows * (D / 4);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float4 v = __ldg(src + size_t(n) * 8 * rows);
+      acc[n].x = fmaf(w, v.x, acc[n].x), acc[n].y = fmaf(w, v.y, acc[n].y);
+      acc[n].z = fmaf(w, v.z, acc[n].z), acc[n].w = fmaf(w, v.w, acc[n].w);
     }
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const size_t row = size_t(q0 + r / p.G) * p.Hq + kvh * p.G + r % p.G;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+  for (int n = 0; n < N; ++n)
+    *reinterpret_cast<uint2*>(out + lane * PITCH + (warp + 8 * n) * 8) =
+        make_uint2(pack_bf16(acc[n].x * inv, acc[n].y * inv),
+                   pack_bf16(acc[n].z * inv, acc[n].w * inv));
+  auto out_row = [&](int i) {
+    return size_t(q0 + i / p.G) * p.Hq + kvh * p.G + i % p.G;
+  };
+  if (warp == 0 && p.lse && row0 + lane < rows)
+    p.lse[out_row(r)] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
+  __syncthreads();
+  constexpr int CPR = D / 8;  // 16-byte pieces of a row
+  for (int i = threadIdx.x; i < 32 * CPR; i += 256) {
+    const int k = i / CPR, c = i % CPR;
+    if (row0 + k < rows)
+      reinterpret_cast<uint4*>(p.o + out_row(row0 + k) * D)[c] =
+          *reinterpret_cast<const uint4*>(out + k * PITCH + c * 16);
+  }
 }
 
 // Opt-in shared memory and the register count of one instantiation, looked up
@@ -926,6 +1029,7 @@ int launch_chunk_d(const ChunkArgs& a) {
   p.kv_indices = a.kv_indices;
   p.n_keys = a.info.n_keys;
   p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
   p.lse = a.lse;
   p.n_rows = a.info.n_rows, p.Hq = a.info.Hq, p.Hkv = a.info.Hkv, p.G = G, p.TPH = TPH;
   p.window = a.info.window;
@@ -939,7 +1043,7 @@ int launch_chunk_d(const ChunkArgs& a) {
   chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, kThreads, C::SMEM, a.stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   if (a.info.n_joins > 0) {
-    const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 7) / 8);
+    const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 31) / 32);
     chunk_join_kernel<D><<<grid, 256, 0, a.stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   }

@@ -22,65 +22,100 @@ constexpr int kTile = psa::kChunkTile;
 // tiles of the same rows, so a tile costs about half as much.  A piece pays
 // for its first tile's latency and its epilogue, a split block for its
 // partial rows and the join launch.
-constexpr double kTwinTile = 0.6, kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.0;
+constexpr double kTwinTile = 0.6, kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
 
 struct Block {
   int32_t q0, ntok, pos0, kv0, lo, hi;  // keys [lo, hi) are seen by some row
   bool twin;
-  int64_t tiles() const { return (int64_t(hi) - lo + kTile - 1) / kTile; }
+  int32_t tiles() const { return int32_t((int64_t(hi) - lo + kTile - 1) / kTile); }
   double tile_cost() const { return twin ? kTwinTile : 1.0; }
-  // pieces for a budget of `len` full tiles per piece
-  int64_t pieces(double len) const {
-    const int64_t per = std::max<int64_t>(1, int64_t(len / tile_cost()));
-    return (tiles() + per - 1) / per;
+  double cost(int32_t n) const {  // of a piece of n tiles
+    return n * tile_cost() + kPieceCost + (n < tiles() || (twin && n > 1) ? kSplitCost : 0.0);
   }
 };
 
+// Tiles [t0, t1) of one block's range for one KV head, in one CTA's list.
 struct Piece {
-  int32_t block, kvh, index;
-  double cost;
+  int32_t block, kvh, t0, t1, cta;
 };
 
-// Longest first, ties in listing order (a KV head's pieces of one key range
-// stay together, so the CTAs in flight share their K/V in L2).
-void list_pieces(const std::vector<Block>& blocks, int32_t Hkv, double len,
-                 const std::vector<int32_t>& first_of_request, std::vector<Piece>& out) {
-  out.clear();
-  for (size_t r = 0; r + 1 < first_of_request.size(); ++r) {
-    const int32_t b0 = first_of_request[r], b1 = first_of_request[r + 1];
-    int64_t most = 0;
-    for (int32_t b = b0; b < b1; ++b) most = std::max(most, blocks[b].pieces(len));
+struct Plan {
+  std::vector<Piece> pieces;  // a CTA's pieces in its order
+  double longest = 0.0;       // cost of the longest list
+};
+
+// Blocks cut into pieces of at most `len` full tiles, handed out longest
+// first to the list that is shortest; ties in listing order (a KV head's
+// pieces of one key range stay together, so the CTAs in flight share their
+// K/V in L2).
+Plan plan_pieces(const std::vector<Block>& blocks, const std::vector<int32_t>& first, int32_t Hkv,
+                 int32_t n_ctas, double len) {
+  Plan plan;
+  auto count = [&](const Block& b) {
+    const int32_t per = int32_t(std::min(1e9, std::max(1.0, len / b.tile_cost())));
+    return (b.tiles() + per - 1) / per;
+  };
+  for (size_t r = 0; r + 1 < first.size(); ++r) {
+    int32_t most = 0;
+    for (int32_t b = first[r]; b < first[r + 1]; ++b) most = std::max(most, count(blocks[b]));
     for (int32_t h = 0; h < Hkv; ++h)
-      for (int64_t s = 0; s < most; ++s)
-        for (int32_t b = b0; b < b1; ++b) {
-          const int64_t n = blocks[b].pieces(len);
-          if (s >= n) continue;
-          const int64_t t = blocks[b].tiles();
-          const int64_t mine = t * (s + 1) / n - t * s / n;
-          const double c = mine * blocks[b].tile_cost() + kPieceCost +
-                           (n > 1 || (blocks[b].twin && t > 1) ? kSplitCost : 0.0);
-          out.push_back({b, h, int32_t(s), c});
+      for (int32_t s = 0; s < most; ++s)
+        for (int32_t b = first[r]; b < first[r + 1]; ++b) {
+          const int64_t n = count(blocks[b]), t = blocks[b].tiles();
+          if (s < n) plan.pieces.push_back({b, h, int32_t(t * s / n), int32_t(t * (s + 1) / n), 0});
         }
   }
-  std::stable_sort(out.begin(), out.end(),
-                   [](const Piece& a, const Piece& b) { return a.cost > b.cost; });
-}
-
-// Greedy assignment; returns the longest list's cost.
-double assign(const std::vector<Piece>& pieces, int32_t n_ctas, std::vector<int32_t>* cta_of) {
+  auto cost = [&](const Piece& p) { return blocks[p.block].cost(p.t1 - p.t0); };
+  std::stable_sort(plan.pieces.begin(), plan.pieces.end(),
+                   [&](const Piece& a, const Piece& b) { return cost(a) > cost(b); });
   using Load = std::pair<double, int32_t>;
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
   for (int32_t c = 0; c < n_ctas; ++c) heap.push({0.0, c});
-  double longest = 0.0;
-  for (size_t i = 0; i < pieces.size(); ++i) {
+  for (Piece& p : plan.pieces) {
     Load l = heap.top();
     heap.pop();
-    if (cta_of) (*cta_of)[i] = l.second;
-    l.first += pieces[i].cost;
-    longest = std::max(longest, l.first);
+    p.cta = l.second;
+    l.first += cost(p);
+    plan.longest = std::max(plan.longest, l.first);
     heap.push(l);
   }
-  return longest;
+  return plan;
+}
+
+// Lists filled one after another up to `budget`, a block cut where a list is
+// full: lists of equal cost with about one cut each.  Returns false if the
+// lists do not hold all.
+bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, double budget,
+                const std::vector<int32_t>& first, Plan& plan) {
+  plan.pieces.clear();
+  plan.longest = 0.0;
+  int32_t cta = 0;
+  double load = 0.0;
+  for (size_t r = 0; r + 1 < first.size(); ++r)
+    for (int32_t h = 0; h < Hkv; ++h)
+      for (int32_t b = first[r]; b < first[r + 1]; ++b) {
+        const Block& k = blocks[b];
+        const int32_t n = k.tiles();
+        for (int32_t t = 0; t < n;) {
+          int32_t fit = n - t;
+          if (load + k.cost(fit) > budget) {
+            const double left = budget - load - kPieceCost - kSplitCost;
+            fit = std::min(n - t, int32_t(left / k.tile_cost()));
+            // no stubs: a cut leaves at least two tiles on both sides
+            if (n - t - fit < 2) fit = n - t - 2;
+            if (fit < 2) {
+              if (load == 0.0 || ++cta == n_ctas) return false;
+              load = 0.0;
+              continue;
+            }
+          }
+          plan.pieces.push_back({b, h, t, t + fit, cta});
+          load += k.cost(fit);
+          plan.longest = std::max(plan.longest, load);
+          t += fit;
+        }
+      }
+  return true;
 }
 
 int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq, int32_t Hkv,
@@ -113,35 +148,62 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
 
   double total = 0.0;
   for (const Block& k : blocks) total += k.tiles() * k.tile_cost() * Hkv;
-  std::vector<Piece> pieces;
-  double best_len = 0.0, best = 0.0;
-  // whole blocks, then pieces of the mean list's length over `rounds`
-  for (double rounds : {0.0, 0.5, 0.6, 0.7, 0.8, 0.9, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5,
-                        4.0, 5.0, 6.0, 7.0, 8.0}) {
-    const double len = rounds == 0 ? 1e18 : std::max(0.5, total / (double(n_ctas) * rounds));
-    int64_t count = 0;
-    double part_rows = 0.0;
-    for (const Block& k : blocks) {
-      const int64_t n = k.pieces(len) * (k.twin ? 2 : 1);
-      count += n * Hkv;
-      if (n > 1) part_rows += double(n) * k.ntok * G * Hkv;
+  // a join reads its partials at memory speed, spread over the CTAs
+  auto join_cost = [&](const Plan& plan) {
+    double rows = 0.0;
+    for (const Piece& p : plan.pieces) {
+      const Block& k = blocks[p.block];
+      if (p.t1 - p.t0 < k.tiles() || (k.twin && k.tiles() > 1))
+        rows += (k.twin ? 2.0 : 1.0) * k.ntok * G;
     }
-    if (rounds > 0 && count > 65536) break;
-    list_pieces(blocks, Hkv, len, first, pieces);
-    // a join reads its partials at memory speed, spread over the CTAs
-    const double c = assign(pieces, n_ctas, nullptr) +
-                     (part_rows > 0.0 ? kJoinCost + part_rows / (n_ctas * 256.0) * 0.25 : 0.0);
-    if (rounds == 0 || c < best) {
-      best = c;
-      best_len = len;
+    return rows > 0.0 ? kJoinCost + rows / (n_ctas * 256.0) * 0.25 : 0.0;
+  };
+  Plan best;
+  double best_cost = 0.0;
+  auto offer = [&](Plan&& plan, double factor = 1.0) {
+    const double c = factor * (plan.longest + join_cost(plan));
+    if (best.pieces.empty() || c < best_cost) {
+      best_cost = c;
+      best = std::move(plan);
     }
-    if (len <= 0.5) break;
+  };
+  if (!blocks.empty()) {
+    // whole blocks, then pieces of the mean list's length over `rounds`
+    for (double rounds : {0.0, 0.5, 0.6, 0.7, 0.8, 0.9, 1.0, 1.25, 1.5, 2.0, 2.5, 3.0, 4.0, 6.0}) {
+      const double len = rounds == 0 ? 1e18 : std::max(0.5, total / (double(n_ctas) * rounds));
+      if (rounds > 0 && blocks.size() * double(Hkv) + total / len > 65536.0) break;
+      offer(plan_pieces(blocks, first, Hkv, n_ctas, len));
+      if (len <= 0.5) break;
+    }
+    // lists of one budget, the smallest that holds all (to 1 %)
+    Plan fill, tried;
+    double low = total / n_ctas, high = 2.0 * low + 8.0;
+    bool found = false;
+    for (int i = 0; i < 24 && (!found || high - low > 0.01 * high); ++i) {
+      const double mid = found || i > 0 ? 0.5 * (low + high) : high;
+      if (fill_lists(blocks, Hkv, n_ctas, mid, first, tried)) {
+        std::swap(fill, tried);
+        high = mid;
+        found = true;
+      } else {
+        low = mid;
+        if (!found) high *= 2.0;
+      }
+    }
+    // Filled lists keep fewer partials, but their CTAs are at different keys
+    // of a head at any time: where the keys and values do not fit L2 they come
+    // from memory more than once.  Measured, pieces against filled lists: 586
+    // and 556 us with 75 MB of keys and values, 454 and 482 us with 290 MB.
+    const double kv_bytes = 4.0 * double(kv0) * Hkv * head_dim;
+    if (found) offer(std::move(fill), kv_bytes > 120e6 ? 1.08 : 1.0);
   }
-  list_pieces(blocks, Hkv, best_len, first, pieces);
-  const int32_t used = int32_t(std::min<int64_t>(n_ctas, std::max<size_t>(1, pieces.size())));
-  std::vector<int32_t> cta_of(pieces.size());
-  assign(pieces, used, &cta_of);
+  const std::vector<Piece>& pieces = best.pieces;
+  int32_t used = 1;
+  for (const Piece& p : pieces) used = std::max(used, p.cta + 1);
 
+  // pieces of each block and head: their partials lie back to back
+  std::vector<int32_t> n_of(blocks.size() * size_t(Hkv), 0);
+  for (const Piece& p : pieces) ++n_of[size_t(p.block) * Hkv + p.kvh];
   // partial rows and joins of the blocks with more than one partial
   std::vector<int64_t> part_of(blocks.size() * size_t(Hkv), -1);
   std::vector<int32_t> joins;
@@ -150,17 +212,17 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
   for (size_t b = 0; b < blocks.size(); ++b) {
     const Block& k = blocks[b];
     const int32_t rows = k.ntok * G;
-    // a twin piece gives two partials (a single tile: the second is empty)
-    const int64_t n = k.pieces(best_len) * (k.twin ? 2 : 1);
-    if (n == 1 || k.tiles() == 1) continue;
     for (int32_t h = 0; h < Hkv; ++h) {
+      // a twin piece gives two partials (a single tile: the second is empty)
+      const int64_t n = int64_t(n_of[b * Hkv + h]) * (k.twin ? 2 : 1);
+      if (n == 1 || k.tiles() == 1) continue;
       part_of[b * Hkv + h] = part_rows;
       const int32_t j[8] = {k.q0, rows, h, int32_t(part_rows), int32_t(n), 0, 0, 0};
       joins.insert(joins.end(), j, j + 8);
       part_rows += n * rows;
       if (part_rows > INT32_MAX) return PSA_ERR_INVALID_ARG;
+      max_join_rows = std::max(max_join_rows, rows);
     }
-    max_join_rows = std::max(max_join_rows, rows);
   }
 
   psa::ChunkPlanView view(used, int32_t(pieces.size()), int32_t(joins.size() / 8));
@@ -177,27 +239,27 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
   out[1] = used;
   out[2] = int32_t(pieces.size());
   out[3] = int32_t(joins.size() / 8);
-  // units in list order: a CTA's pieces keep their longest-first order
+  // units in list order
   std::vector<int32_t> count(used + 1, 0);
-  for (int32_t c : cta_of) ++count[c + 1];
+  for (const Piece& p : pieces) ++count[p.cta + 1];
   for (int32_t c = 0; c < used; ++c) count[c + 1] += count[c];
   std::copy(count.begin(), count.end(), out + view.lists);
-  for (size_t i = 0; i < pieces.size(); ++i) {
-    const Piece& p = pieces[i];
+  std::fill(n_of.begin(), n_of.end(), 0);  // now: partials placed so far
+  for (const Piece& p : pieces) {
     const Block& k = blocks[p.block];
-    const int64_t n = k.pieces(best_len), t = k.tiles();
-    const int64_t t0 = t * p.index / n, t1 = t * (p.index + 1) / n;
-    const int64_t part = part_of[size_t(p.block) * Hkv + p.kvh];
-    int32_t* u = out + view.units + 12 * size_t(count[cta_of[i]]++);
+    const size_t at = size_t(p.block) * Hkv + p.kvh;
+    const int32_t index = n_of[at]++;
+    int32_t* u = out + view.units + 12 * size_t(count[p.cta]++);
     u[0] = k.q0;
     u[1] = k.ntok;
     u[2] = k.pos0;
     u[3] = p.kvh;
     u[4] = k.kv0;
-    u[5] = int32_t(k.lo + t0 * kTile);
-    u[6] = int32_t(std::min<int64_t>(k.lo + t1 * kTile, k.hi));
+    u[5] = k.lo + p.t0 * kTile;
+    u[6] = int32_t(std::min<int64_t>(k.lo + int64_t(p.t1) * kTile, k.hi));
     u[7] = k.twin ? 1 : 0;
-    u[8] = part < 0 ? -1 : int32_t(part + int64_t(p.index) * (k.twin ? 2 : 1) * k.ntok * G);
+    u[8] = part_of[at] < 0 ? -1
+                           : int32_t(part_of[at] + int64_t(index) * (k.twin ? 2 : 1) * k.ntok * G);
   }
   std::copy(joins.begin(), joins.end(), out + view.joins);
   return PSA_OK;
