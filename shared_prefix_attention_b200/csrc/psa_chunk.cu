@@ -58,14 +58,19 @@ namespace {
 
 constexpr int BM = 128;            // query rows per half
 constexpr int BN = kChunkTile;     // keys per tile
-constexpr int kThreads = 384;      // 12 warps
-// Registers: 384 threads x 168 at launch = 64512 = 128 x 104 (loaders, MMA)
-// + 256 x 200 (softmax: a whole 128-column S row in registers).  The launcher
-// checks the compiled count before the first launch.
+constexpr int kParts = 4;          // a tile is loaded in four parts of 32 rows
+// Over a bf16 cache 12 warps, 168 registers a thread at launch = 64512 = 128 x
+// 104 (loaders, MMA) + 256 x 200 (softmax: a whole 128-column S row in
+// registers); the launcher checks the compiled count before the first launch.
+// Over an e4m3 cache 16 warps of 128 registers: widening a tile keeps four
+// loaders busy (two took 2.9 us per tile, more than all else), and the softmax
+// reads its rows in halves.
 constexpr int kRegsLaunch = 168;
 constexpr int kRegsLow = 104, kRegsSoftmax = 200;
-static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
-constexpr int kParts = 4;          // a loader makes a tile in four parts of 32 rows
+template <bool E4M3>
+constexpr int threads() { return E4M3 ? 512 : 384; }
+static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= threads<false>() * kRegsLaunch,
+              "register split");
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
 
@@ -261,12 +266,12 @@ __device__ __forceinline__ float to_log2(float s, const Params& p) {
 // Weights of a row of logits against the max -neg_m, packed in pairs into the
 // row's first half (pair k over logit k <= 2 k, which is done by then);
 // returns their fp32 sum.
-template <bool F16>
-__device__ __forceinline__ float weights_row(uint32_t (&s)[BN], float neg_m, const Params& p) {
+template <bool F16, int N>
+__device__ __forceinline__ float weights_row(uint32_t (&s)[N], float neg_m, const Params& p) {
   const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int k = 0; k < BN / 2; ++k) {
+  for (int k = 0; k < N / 2; ++k) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2, nm2),
               x0, x1);
@@ -335,7 +340,7 @@ __device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_
 }
 
 template <int D, bool E4M3, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<E4M3>(), 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmap_q,
                  const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, Params p) {
@@ -378,11 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_conv, 8);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::NSK; ++i) {
-      mbar_init(k_full + i, 32);
+      mbar_init(k_full + i, E4M3 ? 64 : 32);
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < C::NSV; ++i) {
-      mbar_init(v_full + i, 32);
+      mbar_init(v_full + i, E4M3 ? 64 : 32);
       mbar_init(v_empty + i, 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -402,20 +407,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_slot;
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
-    if (warp == 0 || warp == 2) {
+  if (warp < 4 || warp >= 12) {
+    if constexpr (!E4M3)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
+    if (warp == 0 || warp == 2 || warp == 12 || warp == 13) {
       // ================================================================ loaders
-      // Warp 0 loads K (and the query rows), warp 2 loads V; the rings advance
-      // on their own.  A tile is made in four parts of 32 rows: of the groups
-      // of 8 rows, part v takes the RPI ones at (v % RG) * RPI.  A lane's rows
-      // of a part then all have the same place in the swizzle, so its copies
-      // differ by constant offsets, and one page-table entry per lane covers
-      // the part.
-      const bool is_k = warp == 0;
+      // Warp 0 loads K (and the query rows), warp 2 loads V, over an e4m3 cache
+      // with the help of warps 12 and 13; the rings advance on their own.  A
+      // tile is made in four parts of 32 rows: of the groups of 8 rows, part v
+      // takes the RPI ones at (v % RG) * RPI.  A lane's rows of a part then all
+      // have the same place in the swizzle, so its copies differ by constant
+      // offsets, and one page-table entry per lane covers the part.
+      const bool is_k = warp == 0 || warp == 12;
+      constexpr int MINE = E4M3 ? kParts / 2 : kParts;  // parts of this warp, from v0
+      const int v0 = warp >= 12 ? MINE : 0;
       const int sub = lane / C::CPR, chunk = lane % C::CPR;
       if (lane == 0) {
-        if (is_k) tma_prefetch_desc(&tmap_q);
+        if (warp == 0) tma_prefetch_desc(&tmap_q);
         if (!E4M3 && !p.kv_indices) tma_prefetch_desc(is_k ? &tmap_k : &tmap_v);
       }
       const uint8_t* cache = (is_k ? p.kc : p.vc) + chunk * 16;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int u = u_first - 1, t = 0;
       Unit cur = {};  // the unit of the tile whose rows are at hand
       bool more = true, all = false;
-      int32_t entry[kParts] = {};  // cache rows of this lane's table entries, -1: zeros
+      int32_t entry[MINE] = {};  // cache rows of this lane's table entries, -1: zeros
       const uint8_t* head = nullptr;
       // Moves on to the next tile and reads its page-table entries.
       auto advance = [&]() {
@@ -448,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           head = cache + size_t(cur.kvh) * C::ROWB;
         }
 #pragma unroll
-        for (int v = 0; v < kParts; ++v) {
-          const int pos = t + first_row(v) + lane_row;
+        for (int v = 0; v < MINE; ++v) {
+          const int pos = t + first_row(v0 + v) + lane_row;
           entry[v] = -1;
           if (pos < cur.t1) {
             const int64_t flat = int64_t(cur.kv0) + pos;
@@ -461,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto check = [&]() {
         bool good = true;
 #pragma unroll
-        for (int v = 0; v < kParts; ++v) {
+        for (int v = 0; v < MINE; ++v) {
           if (entry[v] < 0 || entry[v] >= p.n_cache) {
-            if (t + first_row(v) + lane_row < cur.t1) report_status(p.status, PSA_ERR_INVALID_ARG);
+            if (t + first_row(v0 + v) + lane_row < cur.t1) report_status(p.status, PSA_ERR_INVALID_ARG);
             entry[v] = -1;
             good = false;
           }
@@ -488,11 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // e4m3: this lane's staged pieces of a part (16 codes each) to f16
       auto widen_part = [&](int v, uint8_t* dst) {
-        const uint32_t row = uint32_t(first_row(v) + sub), c0 = 2 * (chunk & 3);
+        const uint32_t row = uint32_t(first_row(v0 + v) + sub), c0 = 2 * (chunk & 3);
         dst += uint32_t(chunk >> 2) * (BN * 128);
         uint8_t* at0 = dst + sw128(row, c0);
         uint8_t* at1 = dst + sw128(row, c0 + 1);
-        const uint8_t* src = stage + v * C::NPP * 512;
+        const uint8_t* src = stage + (v0 + v) * C::NPP * 512;
 #pragma unroll
         for (int n = 0; n < C::NPP; ++n) {
           const uint4 w = *reinterpret_cast<const uint4*>(src + n * 512);
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto stage_part = [&](int v) {
-        if (more) copy_part(v, smem_u32(stage) + v * C::NPP * 512, 512);
+        if (more) copy_part(v, smem_u32(stage) + (v0 + v) * C::NPP * 512, 512);
         cp_async_commit();
       };
 
@@ -516,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (E4M3 && more) {
         check();
 #pragma unroll
-        for (int v = 0; v < kParts; ++v) stage_part(v);
+        for (int v = 0; v < MINE; ++v) stage_part(v);
         advance();
       }
       uint32_t slot = 0, phase = 0, uc = 0;
@@ -527,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (E4M3) {
           if (more) check();
 #pragma unroll
-          for (int v = 0; v < kParts; ++v) {
-            cp_async_wait<kParts - 1>();  // this part's copies, the oldest group
+          for (int v = 0; v < MINE; ++v) {
+            cp_async_wait<MINE - 1>();  // this part's copies, the oldest group
             widen_part(v, dst);
             stage_part(v);
           }
@@ -549,13 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             check();
 #pragma unroll
-            for (int v = 0; v < kParts; ++v)
+            for (int v = 0; v < MINE; ++v)
               copy_part(v, smem_u32(dst) + uint32_t(chunk >> 3) * (BN * 128) +
-                               sw128(uint32_t(first_row(v) + sub), chunk & 7), 1024);
+                               sw128(uint32_t(first_row(v0 + v) + sub), chunk & 7), 1024);
             cp_async_arrive(full + slot);
           }
         }
-        if (first && is_k) {
+        if (first && warp == 0) {
           // the query rows, behind the unit's first K tile
           if (lane == 0) {
             ok = mbar_wait(q_empty, (uc & 1) ^ 1, &abort_flag, p.status);
@@ -718,7 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+    if constexpr (!E4M3)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
     // ================================================================ softmax + epilogue
     const int x = (warp - 4) >> 2;      // half
     const int quarter = warp & 3;       // TMEM lane quarter
@@ -780,9 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return m_run == -INFINITY ? 0.f : -m_run;
         };
-        if constexpr (CAP) {
+        if constexpr (CAP || E4M3) {
           // half a row at a time, read twice: a capped weight needs more
-          // registers than a whole row leaves
+          // registers than a whole row leaves, and e4m3 has fewer
           uint32_t sr[BN / 2];
           float mx = -INFINITY;
 #pragma unroll
@@ -797,12 +806,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 2; ++c) {
             tmem_ld64(tS + c * (BN / 2), sr);
             tmem_wait_ld();
-            if (masked) {
-              mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+            if (masked) mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+            if constexpr (!CAP)
+              l_run += weights_row<E4M3>(sr, neg_m, p);
+            else if (masked)
               l_run += weights_row_capped<E4M3, true>(sr, neg_m, p);
-            } else {
+            else
               l_run += weights_row_capped<E4M3, false>(sr, neg_m, p);
-            }
             tmem_st32(tS + c * (BN / 4), *reinterpret_cast<uint32_t(*)[BN / 4]>(sr));
           }
         } else {
@@ -929,7 +939,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
   const int r = min(row0 + lane, rows - 1);
   const float* lse = p.part_lse + a.w + r;
   float m = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < count; ++i) m = fmaxf(m, __ldg(lse + size_t(i) * rows));
   float4 acc[N];
 #pragma unroll
@@ -937,19 +947,31 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
   float sum = 0.f;
   const float4* o0 =
       reinterpret_cast<const float4*>(p.part_o + size_t(a.w) * D) + size_t(warp) * rows + r;
-#pragma unroll 2
-  for (int i = 0; i < count; ++i) {
-    const float l = __ldg(lse + size_t(i) * rows);
-    // an empty partial's rows were not written
-    if (l == -INFINITY) continue;
-    const float w = fast_exp2(l - m);
-    sum += w;
-    const float4* src = o0 + size_t(i) * rows * (D / 4);
+  // four partials at a time, their loads together
+  for (int i0 = 0; i0 < count; i0 += 4) {
+    float l[4];
+    float4 v[4][N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const float4 v = __ldg(src + size_t(n) * 8 * rows);
-      acc[n].x = fmaf(w, v.x, acc[n].x), acc[n].y = fmaf(w, v.y, acc[n].y);
-      acc[n].z = fmaf(w, v.z, acc[n].z), acc[n].w = fmaf(w, v.w, acc[n].w);
+    for (int j = 0; j < 4; ++j) {
+      l[j] = -INFINITY;
+      if (i0 + j < count) {
+        l[j] = __ldg(lse + size_t(i0 + j) * rows);
+        const float4* src = o0 + size_t(i0 + j) * rows * (D / 4);
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[j][n] = __ldg(src + size_t(n) * 8 * rows);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // an empty partial's rows were not written: whatever they hold stays out
+      if (l[j] == -INFINITY) continue;
+      const float w = fast_exp2(l[j] - m);
+      sum += w;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        acc[n].x = fmaf(w, v[j][n].x, acc[n].x), acc[n].y = fmaf(w, v[j][n].y, acc[n].y);
+        acc[n].z = fmaf(w, v[j][n].z, acc[n].z), acc[n].w = fmaf(w, v[j][n].w, acc[n].w);
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -983,7 +1005,7 @@ int prepare_kernel(int dev) {
   cudaFuncAttributes at;
   if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return PSA_ERR_CUDA;
   // setmaxnreg hands out what the launch reserved: fewer would never return
-  if (at.numRegs != kRegsLaunch) return PSA_ERR_UNSUPPORTED;
+  if (!E4M3 && at.numRegs != kRegsLaunch) return PSA_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(Cfg<D, E4M3>::SMEM)) != cudaSuccess)
     return PSA_ERR_CUDA;
@@ -1040,7 +1062,7 @@ int launch_chunk_d(const ChunkArgs& a) {
   p.part_o = a.part_o, p.part_lse = a.part_lse;
   p.part_rows = a.info.part_rows;
   p.status = a.status;
-  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, kThreads, C::SMEM, a.stream>>>(tq, tk, tv, p);
+  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, threads<E4M3>(), C::SMEM, a.stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   if (a.info.n_joins > 0) {
     const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 31) / 32);

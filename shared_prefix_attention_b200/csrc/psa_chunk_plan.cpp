@@ -19,10 +19,10 @@ constexpr int kTile = psa::kChunkTile;
 
 // Costs in units of one 128-key tile of a full block (both 128-row halves).
 // A block whose rows fit one half runs "twin": the halves take alternate
-// tiles of the same rows, so a tile costs about half as much.  A piece pays
+// tiles of the same rows, so a tile costs less (the loaders set its pace).  A piece pays
 // for its first tile's latency and its epilogue, a split block for its
 // partial rows and the join launch.
-constexpr double kTwinTile = 0.6, kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
+constexpr double kTwinTile = 0.8, kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
 
 struct Block {
   int32_t q0, ntok, pos0, kv0, lo, hi;  // keys [lo, hi) are seen by some row
