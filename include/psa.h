@@ -537,7 +537,8 @@ int psa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t
  *             e4m3_scales e4m3 codes of x / scale, saturated at +-448
  *             (a code stands for scale * e4m3, as in psa_verify_fp8_fwd)
  *   dev_slots device int32 [T]: token t's cache row; negative: the token is
- *             padding, nothing of it is cached (its query is still written).
+ *             padding, nothing of it is cached (its query is still written,
+ *             and its position has to be in the table all the same).
  *             A row >= n_cache_tokens sets PSA_ERR_INVALID_ARG in dev_status
  *             and is skipped.  Two tokens with one row race: that row is void.
  *   q_out     device bf16 dense [T, Hq, d] (written)

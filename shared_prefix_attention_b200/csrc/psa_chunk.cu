@@ -285,6 +285,13 @@ __device__ __forceinline__ float weights_row(uint32_t (&s)[N], float neg_m, cons
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
+// min(a, b), NaN if either is (a NaN logit must not become a capped one).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // The same of capped logits.  With e = exp(2 s / c) a weight is 2^(c' - m - 2
 // c' / (1 + e)), c' = c log2(e): two exponentials and a reciprocal, which would
 // leave the special-function unit a third of the uncapped rate.  So four
@@ -307,7 +314,7 @@ __device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_
       float x0, x1;
       f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * k + 2 * j]),
                                __uint_as_float(s[4 * k + 2 * j + 1])), sc2), x0, x1);
-      x0 = fminf(x0, 30.f), x1 = fminf(x1, 30.f);
+      x0 = min_nan(x0, 30.f), x1 = min_nan(x1, 30.f);
       e[j] = f2_pack(fast_exp2(x0), fast_exp2(x1));
     }
     const uint64_t ab = f2_add(e[0], one), cd = f2_add(e[1], one);  // (a, b), (c, d)

@@ -126,3 +126,177 @@ def test_parity(ql, kl, Hq, Hkv, d, paged, kind, window, cap):
     o2, lse2 = psa.chunk(q, k, v, plan, scale, kv_indices=table, logit_cap=cap, k_scale=ks,
                          v_scale=vs)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # every sum has a fixed order
+
+
+def small(seed=1, ql=(100, 3), kl=(700, 300), Hq=8, Hkv=2, d=128, paged=True, kind="bf16", **kw):
+    ql, kl = list(ql), list(kl)
+    q, k, v, ks, vs, table = make(ql, kl, Hq, Hkv, d, paged, kind, seed, **kw)
+    return ql, kl, q, k, v, ks, vs, table, psa.plan_chunk(ql, kl, Hq, Hkv, d)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_bad_pages_read_as_zeros_and_are_reported(kind):
+    """Entries outside the cache (a hole, an index behind the end) in a whole
+    tile and in the last, partial one."""
+    ql, kl, q, k, v, ks, vs, table, plan = small(kind=kind)
+    bad = table.clone()
+    bad[[5, 640, 699, 700, 999]] = torch.tensor([-1, k.shape[0], -2**31, 2**31 - 1, -7],
+                                                dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = psa.chunk(q, k, v, plan, 0.1, kv_indices=bad, k_scale=ks, v_scale=vs, status=st)
+    assert psa.read_status(st) == psa.PSA_ERR_INVALID_ARG
+    kz = torch.cat([values(k, ks), torch.zeros_like(values(k[:1], ks))])
+    vz = torch.cat([values(v, vs), torch.zeros_like(values(v[:1], vs))])
+    at = torch.where((bad < 0) | (bad >= k.shape[0]), k.shape[0], bad)
+    ref = reference(q, kz, vz, ql, kl, at, 0.1, 0, 0.0)
+    check(o, lse, ref, 128, 0.0, 2.0 ** -11 if ks else 2.0 ** -8, "bad pages")
+    # without a status word nothing else changes
+    o2, _ = psa.chunk(q, k, v, plan, 0.1, kv_indices=bad, k_scale=ks, v_scale=vs)
+    assert torch.equal(o, o2)
+
+
+def test_rows_behind_the_last_sequence_are_left_alone():
+    ql, kl, q, k, v, _, _, table, plan = small()
+    qq = torch.cat([q, torch.full((9, 8, 128), float("nan"), dtype=q.dtype, device="cuda")])
+    o = torch.full_like(qq, 7.0)
+    lse = torch.full(qq.shape[:2], 7.0, device="cuda")
+    psa.chunk(qq, k, v, plan, 0.1, kv_indices=table, out=o, lse=lse)
+    want, wl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+    assert torch.equal(o[:-9], want) and torch.equal(lse[:-9], wl)
+    assert (o[-9:] == 7).all() and (lse[-9:] == 7).all()
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_nan_key_reaches_the_rows_that_see_it_and_no_other(cap):
+    ql, kl, q, k, v, _, _, table, plan = small(ql=(300,), kl=(500,))
+    o, lse = psa.chunk(q, k, v, plan, 0.1, kv_indices=table, logit_cap=cap)
+    k[int(table[420])] = float("nan")
+    on, ln = psa.chunk(q, k, v, plan, 0.1, kv_indices=table, logit_cap=cap)
+    assert torch.equal(on[:220], o[:220]) and torch.equal(ln[:220], lse[:220])
+    assert torch.isnan(on[220:].float()).all() and torch.isnan(ln[220:]).all()
+
+
+def test_lowest_logits_and_equal_keys():
+    """Logits far below zero, and rows whose keys are all alike (the mean)."""
+    ql, kl, q, k, v, _, _, table, plan = small()
+    k[:] = -100.0
+    q[:] = 100.0
+    o, lse = psa.chunk(q, k, v, plan, 1.0, kv_indices=table)
+    ref = reference(q, k.double(), v.double(), ql, kl, table, 1.0, 0, 0.0)
+    assert torch.isfinite(o.float()).all()
+    assert float(((o.double() - ref[0]).abs() - 2.0 ** -7 * ref[2]).max()) <= 0
+    # lse = -1.28e6 + log n: a step of fp32 there is 1/8
+    assert float((lse.double() - ref[1]).abs().max()) <= 0.5
+
+
+def test_misaligned_output_and_given_buffers():
+    """Outputs on 16-byte (not 32-byte) boundaries, a caller's workspace."""
+    ql, kl, q, k, v, _, _, table, plan = small(ql=(300,), kl=(300,), paged=False)
+    want, wl = psa.chunk(q, k, v, plan, 0.1)
+    buf = torch.zeros(q.numel() + 8, dtype=q.dtype, device="cuda")
+    o = buf[8:].view(q.shape)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    got, gl = psa.chunk(q, k, v, plan, 0.1, out=o, workspace=ws)
+    assert got.data_ptr() == o.data_ptr() and torch.equal(o, want) and torch.equal(gl, wl)
+    with pytest.raises(psa.PsaError) as e:
+        psa.chunk(q, k, v, plan, 0.1, workspace=ws[:plan.workspace_bytes - 1])
+    assert e.value.status == psa.PSA_ERR_WORKSPACE
+
+
+def test_refused_arguments():
+    ql, kl, q, k, v, ks, vs, table, plan = small()
+    for args in ((q.float(), k, v, plan), (q[:, :4], k, v, plan), (q, k[:, :1], v, plan),
+                 (q, k.float(), v, plan), (q, k.transpose(0, 1), v, plan), (q, k, v[:-1], plan)):
+        with pytest.raises(ValueError):
+            psa.chunk(*args, 0.1, kv_indices=table)
+    with pytest.raises(ValueError):
+        psa.chunk(q, k, v, plan, 0.1, kv_indices=table[:-1])
+    with pytest.raises(ValueError):
+        psa.chunk(q, k, v, plan, 0.1, kv_indices=table.long())
+    for kw in (dict(logit_cap=-1.0), dict(logit_cap=float("inf"))):
+        with pytest.raises(psa.PsaError):
+            psa.chunk(q, k, v, plan, 0.1, kv_indices=table, **kw)
+    with pytest.raises(psa.PsaError):
+        psa.chunk(q, k, v, plan, 0.0, kv_indices=table)
+    with pytest.raises(psa.PsaError):
+        psa.chunk(q, k[:50], v[:50], plan, 0.1)  # no table, and a cache of too few rows
+    with pytest.raises(psa.PsaError):
+        psa.chunk(q[:-1], k, v, plan, 0.1, kv_indices=table)
+
+
+def test_two_graphs_and_an_eager_call_at_once():
+    """Two captured calls replayed on two streams and an eager one on a third,
+    all in flight together; captured replays see new inputs."""
+    sets = [small(seed=s, ql=(200, 64), kl=(3000, 2000)) for s in (1, 2, 3)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for (ql, kl, q, k, v, _, _, table, plan), s in zip(sets[:2], streams):
+        with torch.cuda.stream(s):
+            psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                outs.append(psa.chunk(q, k, v, plan, 0.1, kv_indices=table))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for x in sets:
+        x[2].mul_(-1.5)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            _, _, q, k, v, _, _, table, plan = sets[2]
+            eager = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+    torch.cuda.synchronize()
+    for (ql, kl, q, k, v, _, _, table, plan), got in zip(sets, outs + [eager]):
+        want = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_cache_rows_beyond_32_bit_offsets():
+    """Rows whose byte offsets pass 2^32: appended, attended, read back."""
+    Hq, Hkv, d, n = 4, 2, 128, 130
+    ntok = (1 << 32) // (Hkv * d * 2) + 1000
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.empty(ntok, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rows = (ntok - 1 - torch.randperm(900, generator=g)[:n]).int().cuda()
+    q = torch.randn(n, Hq, d, generator=g).bfloat16().cuda()
+    kn, vn = (torch.randn(n, Hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    assert torch.equal(psa.cache_append(q, kn, vn, k, v, rows), q)
+    kk, vv = psa.cache_read(k, v, rows)
+    assert torch.equal(kk, kn) and torch.equal(vv, vn)
+    plan = psa.plan_chunk([n], [n], Hq, Hkv, d)
+    o, lse = psa.chunk(q, k, v, plan, 0.1, kv_indices=rows)
+    want, wl = psa.chunk(q, kn, vn, plan, 0.1)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+def test_debug_build_agrees():
+    """The bounds-checked library on the same calls."""
+    ql, kl, q, k, v, _, _, table, plan = small()
+    want, wl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with psa.use_library(psa.DEBUG_LIB_PATH):
+        got, gl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table, status=st)
+        torch.cuda.synchronize()
+    assert psa.read_status(st) == 0
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+def test_agrees_with_the_verify_entry():
+    """Draft tokens whose keys are cached already are a chunk: the extend form
+    of verify on the cache without them gives the same rows (two kernels, each
+    within its own bound)."""
+    ql, kl = [4, 2], [900, 130]
+    q, k, v, _, _, _ = make(ql, kl, 8, 2, 128, False, "bf16", 9)
+    o, lse = psa.chunk(q, k, v, psa.plan_chunk(ql, kl, 8, 2, 128), 0.1)
+    new = torch.tensor([896, 897, 898, 899, 1028, 1029], device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.cat([torch.arange(896, **i32), torch.arange(900, 1028, **i32)])
+    o2, lse2 = psa.verify_extend(q, k[new], v[new], k, v, torch.tensor([0, 4, 6], **i32), 4,
+                                 torch.tensor([0, 896, 1024], **i32), 896, 0.1, kv_indices=table)
+    ref = reference(q, k.double(), v.double(), ql, kl, None, 0.1, 0, 0.0)
+    tol = 2 * (2.0 ** -8 * ref[2] + 2.0 ** -8 * ref[0].abs()) + 1e-4
+    assert float(((o.double() - o2.double()).abs() - tol).max()) <= 0
+    assert float((lse - lse2).abs().max()) <= 1e-3
