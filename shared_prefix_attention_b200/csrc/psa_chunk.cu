@@ -266,12 +266,12 @@ __device__ __forceinline__ float to_log2(float s, const Params& p) {
 // Weights of a row of logits against the max -neg_m, packed in pairs into the
 // row's first half (pair k over logit k <= 2 k, which is done by then);
 // returns their fp32 sum.
-template <bool F16, int N>
+template <bool F16, int N, int K0 = 0, int K1 = N / 2>
 __device__ __forceinline__ float weights_row(uint32_t (&s)[N], float neg_m, const Params& p) {
   const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(neg_m, neg_m);
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int k = 0; k < N / 2; ++k) {
+  for (int k = K0; k < K1; ++k) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2, nm2),
               x0, x1);
@@ -628,31 +628,24 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
       auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(b, parity, &abort_flag, p.status));
       };
-      // S_X = Q_X K^T into the S columns of half x
-      auto issue_qk = [&](int x) {
+      // Called by one lane.  S_X = Q_X K^T into the S columns of half x:
+      auto mma_qk = [&](int x) {
         const uint64_t a = dQ + x * (C::Q_BYTES >> 4), b = dK + sk * (C::KV_BYTES >> 4);
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4;
-            umma_ss(tm + x * 256, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
-          }
-          umma_commit(s_full + x);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4;
+          umma_ss(tm + x * 256, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
         }
+        umma_commit(s_full + x);
       };
-      // O_X += P_X V, P_X in TMEM over the first 64 columns of S_X
-      auto issue_pv = [&](int x, bool first) {
+      // O_X += P_X V, P_X in TMEM over the first 64 columns of S_X:
+      auto mma_pv = [&](int x, bool first) {
         const uint64_t b = dV + sv * (C::KV_BYTES >> 4);
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks)
-            umma_ts(tm + x * 256 + 128, tm + x * 256 + ks * 8, b + ks * (2048 >> 4), idesc_pv,
-                    (first && ks == 0) ? 0u : 1u);
-          umma_commit(pv_done + x);
-        }
-      };
-      auto commit = [&](uint64_t* b) {
-        if (elect_one()) umma_commit(b);
+        for (int ks = 0; ks < BN / 16; ++ks)
+          umma_ts(tm + x * 256 + 128, tm + x * 256 + ks * 8, b + ks * (2048 >> 4), idesc_pv,
+                  (first && ks == 0) ? 0u : 1u);
+        umma_commit(pv_done + x);
       };
 
       const int last = __shfl_sync(0xffffffffu, u_end, 0);
@@ -660,64 +653,58 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
         const Unit w = load_unit(p, units, u);
         if (!w.ok) continue;
         const int n = __shfl_sync(0xffffffffu, (w.t1 - w.t0 + BN - 1) / BN, 0);
-        if (!wait(E4M3 ? q_conv : q_full, uc & 1)) {
-          ok = false;
-          break;
-        }
         bool started[2] = {false, false};
         bool see[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           see[x] = __any_sync(0xffffffffu, half_sees(w, x, w.t0, p.TPH, p.window));
-        // the loaders' copies are ordered before the MMAs that read them
-        ok = wait(k_full + sk, kph);
+        ok = wait(k_full + sk, kph) && wait(E4M3 ? q_conv : q_full, uc & 1);
         if (!ok) break;
-        fence_proxy_async_smem();
+        fence_proxy_async_smem();  // the loaders' copies, before the MMAs read them
         tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (see[x]) issue_qk(x);
-        commit(k_empty + sk);
-        if (n == 1) commit(q_empty);
+        if (elect_one()) {
+          if (see[0]) mma_qk(0);
+          if (see[1]) mma_qk(1);
+          umma_commit(k_empty + sk);
+          if (n == 1) umma_commit(q_empty);
+        }
         if (++sk == C::NSK) sk = 0, kph ^= 1;
-        for (int j = 0; j < n && ok; ++j) {
-          bool have_k = false, have_v = false;
+        for (int j = 0; j < n; ++j) {
+          // Everything but P is at hand before P is waited for, so that a
+          // half's PV and its next QK follow its softmax at once.
+          const bool more = j + 1 < n;
+          bool next[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            next[x] = more && __any_sync(0xffffffffu, half_sees(w, x, w.t0 + (j + 1) * BN, p.TPH,
+                                                                p.window));
+          ok = wait(v_full + sv, vph) && (!more || wait(k_full + sk, kph));
+          if (!ok) break;
+          fence_proxy_async_smem();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (ok && see[x]) {
-              ok = wait(p_full + x, pvc[x] & 1) && (have_v || wait(v_full + sv, vph)) &&
-                   (started[x] || wait(o_free + x, (uhc[x] & 1) ^ 1));
+            if (see[x]) {
+              ok = (started[x] || wait(o_free + x, (uhc[x] & 1) ^ 1)) &&
+                   wait(p_full + x, pvc[x] & 1);
               if (!ok) break;
-              if (!have_v) fence_proxy_async_smem();
-              have_v = true;
-              tc_fence_after();
-              issue_pv(x, !started[x]);
-              started[x] = true;
               ++pvc[x];
             }
-            see[x] = j + 1 < n && __any_sync(0xffffffffu, half_sees(w, x, w.t0 + (j + 1) * BN,
-                                                                    p.TPH, p.window));
-            if (ok && see[x]) {
-              if (!have_k) {
-                ok = wait(k_full + sk, kph);
-                if (!ok) break;
-                fence_proxy_async_smem();
-                tc_fence_after();
-                have_k = true;
+            tc_fence_after();
+            if (elect_one()) {
+              if (see[x]) mma_pv(x, !started[x]);
+              if (next[x]) mma_qk(x);
+              if (x == 1) {
+                umma_commit(v_empty + sv);
+                if (more) umma_commit(k_empty + sk);
+                if (j + 2 == n) umma_commit(q_empty);
               }
-              issue_qk(x);
             }
+            started[x] = started[x] || see[x];
+            see[x] = next[x];
           }
           if (!ok) break;
-          if (!have_v) ok = wait(v_full + sv, vph);
-          commit(v_empty + sv);
           if (++sv == C::NSV) sv = 0, vph ^= 1;
-          if (j + 1 < n) {
-            if (!have_k) ok = ok && wait(k_full + sk, kph);
-            commit(k_empty + sk);
-            if (j + 2 == n) commit(q_empty);
-            if (++sk == C::NSK) sk = 0, kph ^= 1;
-          }
+          if (more && ++sk == C::NSK) sk = 0, kph ^= 1;
         }
         if (!ok) break;
 #pragma unroll
@@ -829,8 +816,10 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
           tmem_wait_ld();
           if (masked) mask_row(sr, lo, hi);
           const float neg_m = raise(to_log2<CAP>(max_of_row(sr), p));
-          l_run += weights_row<E4M3>(sr, neg_m, p);
-          tmem_st64(tS, *reinterpret_cast<uint32_t(*)[BN / 2]>(sr));
+          l_run += weights_row<E4M3, BN, 0, BN / 4>(sr, neg_m, p);
+          tmem_st32(tS, *reinterpret_cast<uint32_t(*)[BN / 4]>(sr));
+          l_run += weights_row<E4M3, BN, BN / 4, BN / 2>(sr, neg_m, p);
+          tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[BN / 4]>(sr + BN / 4));
         }
         if (nt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // wait for the latest PV into O, then scale O by alpha in place
