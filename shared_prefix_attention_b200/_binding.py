@@ -661,9 +661,9 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     Tk, Hkv, dk, ks = _rows(k, q.dtype, dev, "k")
     _need(Tk == T and dk == d, "q and k have to agree in tokens and head size")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
-    q_out = (q.new_empty((T, Hq, d)) if q_out is None
+    q_out = (torch.empty_like(q) if q_out is None
              else _dense(q_out, (T, Hq, d), q.dtype, dev, "q_out"))
-    k_out = (q.new_empty((T, Hkv, d)) if k_out is None
+    k_out = (torch.empty_like(k) if k_out is None
              else _dense(k_out, (T, Hkv, d), q.dtype, dev, "k_out"))
     _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks,
             _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how, q_out.data_ptr(),
@@ -688,20 +688,19 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     dqs, dks = Hq * d, Hkv * d
     if dq is None:
-        dq = q.new_empty((T, Hq, d))
+        dq = torch.empty_like(dq_out)
     else:
         _need(dq.shape == q.shape, "dq has to be shaped as q")
         dqs = _rows(dq, q.dtype, dev, "dq")[3]
     if dk is None:
-        dk = q.new_empty((T, Hkv, d))
+        dk = torch.empty_like(dk_out)
     else:
         _need(dk.shape == k.shape, "dk has to be shaped as k")
         dks = _rows(dk, q.dtype, dev, "dk")[3]
-    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dqw = None if q_weight is None else torch.empty_like(q_weight, dtype=torch.float32)
+    dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8,
-                                device=dev)
+        workspace = q.new_empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8)
     _launch("psa_qk_norm_rope_bwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, dq_out.data_ptr(),
             dk_out.data_ptr(), _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how,
             dq.data_ptr(), dqs, dk.data_ptr(), dks, _addr(dqw), _addr(dkw), workspace.data_ptr(),
@@ -751,7 +750,7 @@ def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None,
     if q is not None:
         Tq, Hq, dq, qs = _rows(q, torch.bfloat16, dev, "q")
         _need(Tq == T and dq == d, "q, k and v have to agree in tokens and head size")
-        q_out = (q.new_empty((T, Hq, d)) if q_out is None
+        q_out = (torch.empty_like(q) if q_out is None
                  else _dense(q_out, (T, Hq, d), torch.bfloat16, dev, "q_out"))
     _dense(slots, (T,), torch.int32, dev, "slots")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
@@ -769,9 +768,9 @@ def cache_read(k_cache, v_cache, rows, k_scale: float | None = None,
     ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
     n = rows.numel()
     _dense(rows, (n,), torch.int32, dev, "rows")
-    k = (torch.empty((n, Hkv, d), dtype=torch.bfloat16, device=dev) if k is None
+    k = (k_cache.new_empty((n, Hkv, d), dtype=torch.bfloat16) if k is None
          else _dense(k, (n, Hkv, d), torch.bfloat16, dev, "k"))
-    v = (torch.empty((n, Hkv, d), dtype=torch.bfloat16, device=dev) if v is None
+    v = (torch.empty_like(k) if v is None
          else _dense(v, (n, Hkv, d), torch.bfloat16, dev, "v"))
     _launch("psa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), ntok, rows.data_ptr(),
             n, Hkv, d, sc, k.data_ptr(), v.data_ptr(), _addr(status))
@@ -850,10 +849,10 @@ def chunk(q, k_cache, v_cache, plan: ChunkPlan, scale: float, kv_indices=None,
         _dense(kv_indices, (n,), torch.int32, dev, "kv_indices")
     out = (torch.empty_like(q) if out is None
            else _dense(out, (T, Hq, d), torch.bfloat16, dev, "out"))
-    lse = (torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None
+    lse = (q.new_empty((T, Hq), dtype=torch.float32) if lse is None
            else _dense(lse, (T, Hq), torch.float32, dev, "lse"))
     if workspace is None:
-        workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(plan.workspace_bytes, dtype=torch.uint8)
     _launch("psa_chunk_fwd", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ntok,
             _addr(kv_indices), sc, out.data_ptr(), lse.data_ptr(), T, scale, logit_cap, plan._ref,
             plan.data.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status))

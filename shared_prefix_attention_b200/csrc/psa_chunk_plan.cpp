@@ -37,6 +37,7 @@ struct Block {
 // Tiles [t0, t1) of one block's range for one KV head, in one CTA's list.
 struct Piece {
   int32_t block, kvh, t0, t1, cta;
+  float cost;
 };
 
 struct Plan {
@@ -55,29 +56,41 @@ Plan plan_pieces(const std::vector<Block>& blocks, const std::vector<int32_t>& f
     const int32_t per = int32_t(std::min(1e9, std::max(1.0, len / b.tile_cost())));
     return (b.tiles() + per - 1) / per;
   };
+  // the KV heads are alike: list and sort one head's pieces, then repeat them
+  std::vector<Piece> one;
   for (size_t r = 0; r + 1 < first.size(); ++r) {
     int32_t most = 0;
     for (int32_t b = first[r]; b < first[r + 1]; ++b) most = std::max(most, count(blocks[b]));
-    for (int32_t h = 0; h < Hkv; ++h)
-      for (int32_t s = 0; s < most; ++s)
-        for (int32_t b = first[r]; b < first[r + 1]; ++b) {
-          const int64_t n = count(blocks[b]), t = blocks[b].tiles();
-          if (s < n) plan.pieces.push_back({b, h, int32_t(t * s / n), int32_t(t * (s + 1) / n), 0});
-        }
+    for (int32_t s = 0; s < most; ++s)
+      for (int32_t b = first[r]; b < first[r + 1]; ++b) {
+        const int64_t n = count(blocks[b]), t = blocks[b].tiles();
+        if (s >= n) continue;
+        const int32_t t0 = int32_t(t * s / n), t1 = int32_t(t * (s + 1) / n);
+        one.push_back({b, 0, t0, t1, 0, float(blocks[b].cost(t1 - t0))});
+      }
   }
-  auto cost = [&](const Piece& p) { return blocks[p.block].cost(p.t1 - p.t0); };
-  std::stable_sort(plan.pieces.begin(), plan.pieces.end(),
-                   [&](const Piece& a, const Piece& b) { return cost(a) > cost(b); });
+  std::stable_sort(one.begin(), one.end(),
+                   [](const Piece& a, const Piece& b) { return a.cost > b.cost; });
+  // lists by (load, number), the shortest on top
   using Load = std::pair<double, int32_t>;
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
   for (int32_t c = 0; c < n_ctas; ++c) heap.push({0.0, c});
-  for (Piece& p : plan.pieces) {
-    Load l = heap.top();
-    heap.pop();
-    p.cta = l.second;
-    l.first += cost(p);
-    plan.longest = std::max(plan.longest, l.first);
-    heap.push(l);
+  plan.pieces.reserve(one.size() * size_t(Hkv));
+  // pieces of one cost, head by head
+  for (size_t i = 0, j = 0; i < one.size(); i = j) {
+    while (j < one.size() && one[j].cost == one[i].cost) ++j;
+    for (int32_t h = 0; h < Hkv; ++h)
+      for (size_t k = i; k < j; ++k) {
+        Piece p = one[k];
+        Load l = heap.top();
+        heap.pop();
+        p.kvh = h;
+        p.cta = l.second;
+        l.first += p.cost;
+        plan.longest = std::max(plan.longest, l.first);
+        heap.push(l);
+        plan.pieces.push_back(p);
+      }
   }
   return plan;
 }
@@ -109,7 +122,7 @@ bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, d
               continue;
             }
           }
-          plan.pieces.push_back({b, h, t, t + fit, cta});
+          plan.pieces.push_back({b, h, t, t + fit, cta, 0.f});
           load += k.cost(fit);
           plan.longest = std::max(plan.longest, load);
           t += fit;
@@ -169,7 +182,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
   };
   if (!blocks.empty()) {
     // whole blocks, then pieces of the mean list's length over `rounds`
-    for (double rounds : {0.0, 0.5, 0.6, 0.7, 0.8, 0.9, 1.0, 1.25, 1.5, 2.0, 2.5, 3.0, 4.0, 6.0}) {
+    for (double rounds : {0.0, 0.5, 0.75, 1.0, 1.5, 1.75, 2.0, 2.5, 3.0}) {
       const double len = rounds == 0 ? 1e18 : std::max(0.5, total / (double(n_ctas) * rounds));
       if (rounds > 0 && blocks.size() * double(Hkv) + total / len > 65536.0) break;
       offer(plan_pieces(blocks, first, Hkv, n_ctas, len));
@@ -179,7 +192,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
     Plan fill, tried;
     double low = total / n_ctas, high = 2.0 * low + 8.0;
     bool found = false;
-    for (int i = 0; i < 24 && (!found || high - low > 0.01 * high); ++i) {
+    for (int i = 0; i < 20 && (!found || high - low > 0.01 * high); ++i) {
       const double mid = found || i > 0 ? 0.5 * (low + high) : high;
       if (fill_lists(blocks, Hkv, n_ctas, mid, first, tried)) {
         std::swap(fill, tried);
