@@ -51,6 +51,7 @@
 #include "psa_debug.cuh"
 #include "psa_device.cuh"
 #include "psa_internal.h"
+#include "psa_pair.cuh"
 #include "psa_tmem_wide.cuh"
 
 namespace psa {
