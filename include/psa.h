@@ -576,6 +576,8 @@ typedef struct psa_chunk_info {
     int32_t n_units;    /* pieces of work */
     int32_t n_joins;    /* query blocks whose keys are split over several units */
     int32_t max_join_rows;  /* query rows of the largest such block */
+    int32_t all_twin;   /* 1: every query block fits 128 rows (few new tokens) */
+    int32_t reserved;
     int64_t n_keys;     /* key positions of all requests */
     int64_t part_rows;  /* rows of partial results */
     int64_t len;        /* int32 words of the plan */

@@ -88,7 +88,8 @@ class ChunkInfo(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("n_rows", ctypes.c_int32), ("n_ctas", ctypes.c_int32),
                 ("n_units", ctypes.c_int32), ("n_joins", ctypes.c_int32),
-                ("max_join_rows", ctypes.c_int32), ("n_keys", ctypes.c_int64),
+                ("max_join_rows", ctypes.c_int32), ("all_twin", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("n_keys", ctypes.c_int64),
                 ("part_rows", ctypes.c_int64), ("len", ctypes.c_int64)]
 
 

@@ -16,27 +16,33 @@
 // halves on one K/V tile stream, or, where the rows fit one half ("twin"),
 // with both halves on the same rows and alternate tiles: then each half keeps
 // its own running max and sum and writes its own partial.
-//   warps 0, 2   loaders of K (and the query rows, by TMA) and of V.  A page
-//                table scatters a tile's keys, so their rows are gathered with
-//                16-byte asynchronous copies straight into the 128-byte-
-//                swizzled tiles the MMA reads, zeros behind the key range (no
-//                unused cache row is touched); whole tiles of a contiguous
-//                bf16 range come by TMA.  e4m3 rows go through a thread-
-//                private staging area and are widened to f16 (exact) by the
-//                thread that copied them.  The loaders share their schedulers
-//                with the softmax warps, which leave few issue slots: an
-//                earlier form that computed each copy's addresses took 7500
-//                cycles per tile where this one takes under 3000 (four-row
-//                TMA gathers move half as much as these copies: 21 against 41
-//                bytes per clock and SM).
+//   warps 0, 2   loaders of K (and the query rows, by TMA) and of V, in the
+//                wide form with two more each.  A page table scatters a tile's
+//                keys, so their rows are gathered with 16-byte asynchronous
+//                copies straight into the 128-byte-swizzled tiles the MMA
+//                reads, zeros behind the key range (no unused cache row is
+//                touched); whole tiles of a contiguous bf16 range come by TMA.
+//                e4m3 rows go through a thread-private staging area and are
+//                widened to f16 (exact) by the thread that copied them.  The
+//                loaders share their schedulers with the softmax warps, which
+//                leave few issue slots: an earlier form that computed each
+//                copy's addresses took 7500 cycles per tile where this one
+//                takes under 3000 (four-row TMA gathers move half as much as
+//                these copies: 21 against 41 bytes per clock and SM).
 //   warp 1       tcgen05 issuer: per half S = Q K^T into TMEM, O += P V with P
 //                read from TMEM over the S columns.  The whole warp walks in
 //                step so that descriptors stay in uniform registers (a single
-//                lane in a divergent branch issued at half the rate).
+//                lane in a divergent branch issued at half the rate), and
+//                waits for everything but P first.
 //   warps 4..11  softmax of the two halves, one row per thread, running max in
 //                the log2 domain with lazy rescaling, and the epilogue: final
 //                rows, or a partial (O / l and log2-sum-exp, fp32) for the
 //                join kernel.
+// What bounds it (one long prompt's piece, 2048 tokens over 16k keys, 480 us =
+// 1.2 PFLOP/s, SM clock 1.66 GHz under the power limit): the special-function
+// unit and the tensor pipe are each busy 60 % of the time; a tile's chain QK,
+// softmax, PV (about 3400 cycles) is longer than either's share of it (2050),
+// and two halves are all that TMEM holds.
 // P is rounded to bf16 (f16 over an e4m3 cache) for the tensor cores: at most
 // half a step per weight, averaged over the keys; the sum l keeps fp32.
 // Every wait is bounded.
@@ -59,23 +65,22 @@ namespace {
 
 constexpr int BM = 128;            // query rows per half
 constexpr int BN = kChunkTile;     // keys per tile
-constexpr int kParts = 4;          // a tile is loaded in four parts of 32 rows
-// Over a bf16 cache 12 warps, 168 registers a thread at launch = 64512 = 128 x
+// The narrow form: 12 warps, 168 registers a thread at launch = 64512 = 128 x
 // 104 (loaders, MMA) + 256 x 200 (softmax: a whole 128-column S row in
 // registers); the launcher checks the compiled count before the first launch.
-// Over an e4m3 cache 16 warps of 128 registers: widening a tile keeps four
-// loaders busy (two took 2.9 us per tile, more than all else), and the softmax
+// The wide form: 16 warps of 128 registers, more loaders, and a softmax that
 // reads its rows in halves.
 constexpr int kRegsLaunch = 168;
 constexpr int kRegsLow = 104, kRegsSoftmax = 200;
-template <bool E4M3>
-constexpr int threads() { return E4M3 ? 512 : 384; }
+constexpr int kWideLoaders = 3, kWideParts = 8;
+template <bool WIDE>
+constexpr int threads() { return WIDE ? 512 : 384; }
 static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= threads<false>() * kRegsLaunch,
               "register split");
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool WIDE>
 struct Cfg {
   static constexpr int NPART = D / 64;  // 128-byte swizzle atoms across d
   static constexpr uint32_t Q_BYTES = BM * D * 2;  // one half
@@ -84,7 +89,10 @@ struct Cfg {
   static constexpr int CPR = ROWB / 16;            // 16-byte copies of a row
   static constexpr int RPI = 32 / CPR;             // rows per warp instruction
   static constexpr int RG = 8 / RPI;               // instructions per 8 rows
-  static constexpr int NPP = BN / 8 * RG / kParts;  // instructions per part
+  static constexpr int PARTS = WIDE ? kWideParts : 4;  // a tile is loaded in parts
+  static constexpr int NPP = BN / 8 * RG / PARTS;  // instructions per part
+  static constexpr int LOADERS = WIDE ? kWideLoaders : 1;  // warps of K, and of V
+  static constexpr int MINE = (PARTS + LOADERS - 1) / LOADERS;  // parts of a warp at most
   static constexpr uint32_t STAGE_BYTES = E4M3 ? BN * D : 0;  // raw K (or V) tile
   static constexpr int NSK = D == 64 ? 4 : (E4M3 ? 2 : 3);
   static constexpr int NSV = D == 64 ? 4 : 2;
@@ -347,12 +355,12 @@ __device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_
   return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
-template <int D, bool E4M3, bool CAP>
-__global__ void __launch_bounds__(threads<E4M3>(), 1)
+template <int D, bool E4M3, bool CAP, bool WIDE>
+__global__ void __launch_bounds__(threads<WIDE>(), 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmap_q,
                  const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, Params p) {
-  using C = Cfg<D, E4M3>;
+  using C = Cfg<D, E4M3, WIDE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -391,11 +399,11 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
     mbar_init(q_conv, 8);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::NSK; ++i) {
-      mbar_init(k_full + i, E4M3 ? 64 : 32);
+      mbar_init(k_full + i, C::LOADERS * 32);
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < C::NSV; ++i) {
-      mbar_init(v_full + i, E4M3 ? 64 : 32);
+      mbar_init(v_full + i, C::LOADERS * 32);
       mbar_init(v_empty + i, 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -416,19 +424,19 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
   const uint32_t tmem = tmem_base_slot;
 
   if (warp < 4 || warp >= 12) {
-    if constexpr (!E4M3)
+    if constexpr (!WIDE)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
-    if (warp == 0 || warp == 2 || warp == 12 || warp == 13) {
+    if (warp == 0 || warp == 2 || (warp >= 12 && warp < 10 + 2 * C::LOADERS)) {
       // ================================================================ loaders
-      // Warp 0 loads K (and the query rows), warp 2 loads V, over an e4m3 cache
-      // with the help of warps 12 and 13; the rings advance on their own.  A
-      // tile is made in four parts of 32 rows: of the groups of 8 rows, part v
-      // takes the RPI ones at (v % RG) * RPI.  A lane's rows of a part then all
-      // have the same place in the swizzle, so its copies differ by constant
+      // Warp 0 loads K (and the query rows), warp 2 loads V, in the wide form
+      // with the help of warps 12, 14 and 13, 15; the rings advance on their
+      // own.  A tile is made in parts: of the groups of 8 rows, part v takes
+      // the RPI ones at (v % RG) * RPI.  A lane's rows of a part then all have
+      // the same place in the swizzle, so its copies differ by constant
       // offsets, and one page-table entry per lane covers the part.
-      const bool is_k = warp == 0 || warp == 12;
-      constexpr int MINE = E4M3 ? kParts / 2 : kParts;  // parts of this warp, from v0
-      const int v0 = warp >= 12 ? MINE : 0;
+      const bool is_k = (warp & 1) == 0 && warp != 2;
+      const int v0 = (warp < 12 ? 0 : (warp - 10) / 2) * C::MINE;
+      const int n_mine = min(C::MINE, C::PARTS - v0);
       const int sub = lane / C::CPR, chunk = lane % C::CPR;
       if (lane == 0) {
         if (warp == 0) tma_prefetch_desc(&tmap_q);
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
       int u = u_first - 1, t = 0;
       Unit cur = {};  // the unit of the tile whose rows are at hand
       bool more = true, all = false;
-      int32_t entry[MINE] = {};  // cache rows of this lane's table entries, -1: zeros
+      int32_t entry[C::MINE] = {};  // cache rows of this lane's table entries, -1: zeros
       const uint8_t* head = nullptr;
       // Moves on to the next tile and reads its page-table entries.
       auto advance = [&]() {
@@ -464,10 +472,10 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
           head = cache + size_t(cur.kvh) * C::ROWB;
         }
 #pragma unroll
-        for (int v = 0; v < MINE; ++v) {
+        for (int v = 0; v < C::MINE; ++v) {
           const int pos = t + first_row(v0 + v) + lane_row;
           entry[v] = -1;
-          if (pos < cur.t1) {
+          if (v < n_mine && lane < C::NPP * C::RPI && pos < cur.t1) {
             const int64_t flat = int64_t(cur.kv0) + pos;
             entry[v] = p.kv_indices ? __ldg(p.kv_indices + flat) : int32_t(flat);
           }
@@ -477,8 +485,8 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
       auto check = [&]() {
         bool good = true;
 #pragma unroll
-        for (int v = 0; v < MINE; ++v) {
-          if (entry[v] < 0 || entry[v] >= p.n_cache) {
+        for (int v = 0; v < C::MINE; ++v) {
+          if (v < n_mine && lane < C::NPP * C::RPI && (entry[v] < 0 || entry[v] >= p.n_cache)) {
             if (t + first_row(v0 + v) + lane_row < cur.t1) report_status(p.status, PSA_ERR_INVALID_ARG);
             entry[v] = -1;
             good = false;
@@ -532,7 +540,8 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
       if (E4M3 && more) {
         check();
 #pragma unroll
-        for (int v = 0; v < MINE; ++v) stage_part(v);
+        for (int v = 0; v < C::MINE; ++v)
+          if (v < n_mine) stage_part(v);
         advance();
       }
       uint32_t slot = 0, phase = 0, uc = 0;
@@ -543,8 +552,13 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
         if constexpr (E4M3) {
           if (more) check();
 #pragma unroll
-          for (int v = 0; v < MINE; ++v) {
-            cp_async_wait<MINE - 1>();  // this part's copies, the oldest group
+          for (int v = 0; v < C::MINE; ++v) {
+            if (v >= n_mine) break;
+            // this part's copies: the oldest group
+            if (n_mine == C::MINE)
+              cp_async_wait<C::MINE - 1>();
+            else
+              cp_async_wait<C::MINE - 2>();
             widen_part(v, dst);
             stage_part(v);
           }
@@ -553,7 +567,7 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
         } else {
           if (!p.kv_indices && t + BN <= cur.t1) {
             // a whole tile of a contiguous range: one TMA copy
-            if (lane == 0) {
+            if (lane == 0 && warp < 12) {
               mbar_arrive_expect_tx(full + slot, C::KV_BYTES);
 #pragma unroll
               for (int part = 0; part < C::NPART; ++part)
@@ -565,9 +579,10 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
           } else {
             check();
 #pragma unroll
-            for (int v = 0; v < MINE; ++v)
-              copy_part(v, smem_u32(dst) + uint32_t(chunk >> 3) * (BN * 128) +
-                               sw128(uint32_t(first_row(v0 + v) + sub), chunk & 7), 1024);
+            for (int v = 0; v < C::MINE; ++v)
+              if (v < n_mine)
+                copy_part(v, smem_u32(dst) + uint32_t(chunk >> 3) * (BN * 128) +
+                                 sw128(uint32_t(first_row(v0 + v) + sub), chunk & 7), 1024);
             cp_async_arrive(full + slot);
           }
         }
@@ -654,6 +669,7 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
         const Unit w = load_unit(p, units, u);
         if (!w.ok) continue;
         const int n = __shfl_sync(0xffffffffu, (w.t1 - w.t0 + BN - 1) / BN, 0);
+        const bool twin = __any_sync(0xffffffffu, w.twin);
         bool started[2] = {false, false};
         bool see[2];
 #pragma unroll
@@ -682,6 +698,11 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
           ok = wait(v_full + sv, vph) && (!more || wait(k_full + sk, kph));
           if (!ok) break;
           fence_proxy_async_smem();
+          // the other half of a twin has no P to come: it starts at once
+          if (twin && more) {
+            tc_fence_after();
+            if (elect_one()) mma_qk(next[1]);
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (see[x]) {
@@ -693,7 +714,7 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
             tc_fence_after();
             if (elect_one()) {
               if (see[x]) mma_pv(x, !started[x]);
-              if (next[x]) mma_qk(x);
+              if (next[x] && !twin) mma_qk(x);
               if (x == 1) {
                 umma_commit(v_empty + sv);
                 if (more) umma_commit(k_empty + sk);
@@ -721,7 +742,7 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
       }
     }
   } else {
-    if constexpr (!E4M3)
+    if constexpr (!WIDE)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
     // ================================================================ softmax + epilogue
     const int x = (warp - 4) >> 2;      // half
@@ -784,9 +805,9 @@ __global__ void __launch_bounds__(threads<E4M3>(), 1)
           }
           return m_run == -INFINITY ? 0.f : -m_run;
         };
-        if constexpr (CAP || E4M3) {
+        if constexpr (CAP || WIDE) {
           // half a row at a time, read twice: a capped weight needs more
-          // registers than a whole row leaves, and e4m3 has fewer
+          // registers than a whole row leaves, and the wide form has fewer
           uint32_t sr[BN / 2];
           float mx = -INFINITY;
 #pragma unroll
@@ -994,28 +1015,28 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
 
 // Opt-in shared memory and the register count of one instantiation, looked up
 // once per device.
-template <int D, bool E4M3, bool CAP>
+template <int D, bool E4M3, bool CAP, bool WIDE>
 int prepare_kernel(int dev) {
   static std::atomic<uint64_t> done{0};
   if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return PSA_OK;
-  auto kern = chunk_kernel<D, E4M3, CAP>;
+  auto kern = chunk_kernel<D, E4M3, CAP, WIDE>;
   cudaFuncAttributes at;
   if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return PSA_ERR_CUDA;
   // setmaxnreg hands out what the launch reserved: fewer would never return
-  if (!E4M3 && at.numRegs != kRegsLaunch) return PSA_ERR_UNSUPPORTED;
+  if (!WIDE && at.numRegs != kRegsLaunch) return PSA_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           int(Cfg<D, E4M3>::SMEM)) != cudaSuccess)
+                           int(Cfg<D, E4M3, WIDE>::SMEM)) != cudaSuccess)
     return PSA_ERR_CUDA;
   if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   return PSA_OK;
 }
 
-template <int D, bool E4M3, bool CAP>
+template <int D, bool E4M3, bool CAP, bool WIDE>
 int launch_chunk_d(const ChunkArgs& a) {
-  using C = Cfg<D, E4M3>;
+  using C = Cfg<D, E4M3, WIDE>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PSA_ERR_CUDA;
-  int rc = prepare_kernel<D, E4M3, CAP>(dev);
+  int rc = prepare_kernel<D, E4M3, CAP, WIDE>(dev);
   if (rc != PSA_OK) return rc;
   const int G = a.info.Hq / a.info.Hkv, TPH = BM / G;
   CUtensorMap tq;
@@ -1059,7 +1080,7 @@ int launch_chunk_d(const ChunkArgs& a) {
   p.part_o = a.part_o, p.part_lse = a.part_lse;
   p.part_rows = a.info.part_rows;
   p.status = a.status;
-  chunk_kernel<D, E4M3, CAP><<<a.info.n_ctas, threads<E4M3>(), C::SMEM, a.stream>>>(tq, tk, tv, p);
+  chunk_kernel<D, E4M3, CAP, WIDE><<<a.info.n_ctas, threads<WIDE>(), C::SMEM, a.stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   if (a.info.n_joins > 0) {
     const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 31) / 32);
@@ -1069,11 +1090,23 @@ int launch_chunk_d(const ChunkArgs& a) {
   return PSA_OK;
 }
 
+template <int D, bool E4M3, bool WIDE>
+int launch_chunk_cap(const ChunkArgs& a) {
+  return a.cap > 0.f ? launch_chunk_d<D, E4M3, true, WIDE>(a)
+                     : launch_chunk_d<D, E4M3, false, WIDE>(a);
+}
+
 template <int D>
 int launch_chunk_of(const ChunkArgs& a) {
-  if (a.e4m3)
-    return a.cap > 0.f ? launch_chunk_d<D, true, true>(a) : launch_chunk_d<D, true, false>(a);
-  return a.cap > 0.f ? launch_chunk_d<D, false, true>(a) : launch_chunk_d<D, false, false>(a);
+  // The wide form over an e4m3 cache (widening a tile keeps the loaders busy:
+  // 418 us against 311 for pieces of 1024 tokens over 8k histories), and for
+  // few rows through a page table, where gathering sets the pace (18 requests'
+  // single tokens over 16k keys: 243 us against 211; contiguous, by TMA, 186
+  // against 188).  For full blocks over bf16 its softmax costs more than its
+  // loaders gain: 410 us against 425 on 16k paged histories.
+  if (a.e4m3) return launch_chunk_cap<D, true, true>(a);
+  return a.info.all_twin && a.kv_indices ? launch_chunk_cap<D, false, true>(a)
+                                         : launch_chunk_cap<D, false, false>(a);
 }
 
 }  // namespace

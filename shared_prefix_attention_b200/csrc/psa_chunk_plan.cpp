@@ -239,13 +239,14 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
   }
 
   psa::ChunkPlanView view(used, int32_t(pieces.size()), int32_t(joins.size() / 8));
-  *info = psa_chunk_info{B,    Hq,
-                         Hkv,  head_dim,
-                         window, int32_t(q0),
-                         used, int32_t(pieces.size()),
-                         int32_t(joins.size() / 8), max_join_rows,
-                         kv0,  part_rows,
-                         view.len};
+  *info = {};
+  info->B = B, info->Hq = Hq, info->Hkv = Hkv, info->head_dim = head_dim, info->window = window;
+  info->n_rows = int32_t(q0), info->n_keys = kv0;
+  info->n_ctas = used, info->n_units = int32_t(pieces.size());
+  info->n_joins = int32_t(joins.size() / 8), info->max_join_rows = max_join_rows;
+  info->all_twin =
+      std::all_of(blocks.begin(), blocks.end(), [](const Block& k) { return k.twin; });
+  info->part_rows = part_rows, info->len = view.len;
   if (!out || cap < view.len) return PSA_ERR_CAPACITY;
   std::fill(out, out + view.len, 0);
   out[0] = psa::kChunkMagic;
