@@ -593,7 +593,7 @@ typedef struct psa_chunk_info {
  * `window` keys only (itself included); 0: all.
  * out: the plan, to be copied to 16-byte aligned device memory; PSA_ERR_CAPACITY (with
  * info->len set) if cap is smaller.  PSA_ERR_INVALID_ARG for a negative length,
- * kv_lens[b] < qo_lens[b], or totals beyond 2^31 - 1; PSA_ERR_UNSUPPORTED for a
+ * kv_lens[b] < qo_lens[b], or totals beyond 2^31 - 257; PSA_ERR_UNSUPPORTED for a
  * head_dim other than 64 or 128 or Hq / Hkv above 128. */
 int psa_build_chunk_plan(const int32_t *qo_lens, const int32_t *kv_lens, int32_t B, int32_t Hq,
                          int32_t Hkv, int32_t head_dim, int32_t window, int32_t n_ctas,
@@ -613,7 +613,9 @@ size_t psa_chunk_workspace_size(const psa_chunk_info *info);
  *              a row outside the cache reads as zeros and sets
  *              PSA_ERR_INVALID_ARG in dev_status
  *   logit_cap  0: none; c > 0: logits become c tanh(logit / c) before the mask
- *   o          device [T, Hq, d] bf16 (written up to n_rows)
+ *              (c <= 1000, PSA_ERR_UNSUPPORTED above: the cap is formed with an
+ *              error of about 2^-22 c)
+ *   o          device [T, Hq, d] bf16 (written up to n_rows; may not overlap q)
  *   lse        device [T, Hq] fp32 (written up to n_rows; nullable)
  * Token i of request b is at position kv_lens[b] - qo_lens[b] + i and sees the
  * keys up to its own position, the last `window` of them if the plan has a

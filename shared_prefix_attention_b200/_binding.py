@@ -567,8 +567,9 @@ def verify_extend(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr: torch.
 # Short forms of torch.cuda.current_device() and current_stream().cuda_stream:
 # a decoding step's calls take a few microseconds on the GPU, so every
 # microsecond of the host's part counts.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch(name: str, device, *args):
@@ -627,6 +628,8 @@ def _norm_rope(T: int, d: int, device, positions, cos_sin, q_weight, k_weight, e
             raise ValueError("cos_sin: [positions, rot_dim] is needed")
         pos = _dense(positions, (T,), torch.int32, device, "positions").data_ptr()
         n_pos, rot = cos_sin.shape
+        if n_pos == 0:
+            raise ValueError("cos_sin: at least one position is needed")
         cs = _dense(cos_sin, (n_pos, rot), torch.float32, device, "cos_sin").data_ptr()
     if q_weight is not None:
         wdt = _weight_dtype(q_weight, "q_weight")

@@ -517,9 +517,9 @@ bool ok_stride(int64_t stride, int32_t H, int32_t d, int elem) {
   return stride >= int64_t(H) * d && (stride * elem) % 16 == 0;
 }
 
-bool ok_how(const psa_norm_rope* how, int32_t d) {
+bool ok_how(const psa_norm_rope* how, int32_t d, int32_t T) {
   if (how->cos_sin) {
-    if (!how->positions || how->n_positions < 0 || how->rot_dim <= 0 || how->rot_dim > d ||
+    if ((T > 0 && !how->positions) || how->n_positions < 0 || how->rot_dim <= 0 || how->rot_dim > d ||
         how->rot_dim % 16 != 0 || !aligned16(how->cos_sin) ||
         (reinterpret_cast<uintptr_t>(how->positions) & 3u))
       return false;
@@ -547,7 +547,7 @@ extern "C" int psa_qk_norm_rope_fwd(const void* q, int64_t q_stride, const void*
       (T > 0 && !q && !k) || (q && Hq <= 0) || (k && Hkv <= 0))
     return PSA_ERR_INVALID_ARG;
   if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
-  if (!ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  if (!ok_how(how, head_dim, T)) return PSA_ERR_INVALID_ARG;
   if (T == 0) return PSA_OK;
   const int elem = dtype == PSA_F32 ? 4 : 2;
   if ((q && (!q_out || !aligned16(q) || !aligned16(q_out) ||
@@ -582,7 +582,7 @@ extern "C" int psa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void*
       (T > 0 && !q && !k) || (q && Hq <= 0) || (k && Hkv <= 0))
     return PSA_ERR_INVALID_ARG;
   if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
-  if (!ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  if (!ok_how(how, head_dim, T)) return PSA_ERR_INVALID_ARG;
   // a weight gradient needs the norm it belongs to
   if ((dq_weight && !how->q_weight) || (dk_weight && !how->k_weight) ||
       (T > 0 && ((dq_weight && !q) || (dk_weight && !k))) ||
@@ -626,7 +626,11 @@ extern "C" int psa_cache_append(const void* q, int64_t q_stride, const void* k, 
       !ok_scales(e4m3_scales))
     return PSA_ERR_INVALID_ARG;
   if (!ok_head_dim(head_dim)) return PSA_ERR_UNSUPPORTED;
-  if (how && !ok_how(how, head_dim)) return PSA_ERR_INVALID_ARG;
+  if (how && !ok_how(how, head_dim, T)) return PSA_ERR_INVALID_ARG;
+  // codes are rounded from x * (1 / scale)
+  if (e4m3_scales && (!std::isfinite(1.f / e4m3_scales->k_scale) ||
+                      !std::isfinite(1.f / e4m3_scales->v_scale)))
+    return PSA_ERR_INVALID_ARG;
   if (T == 0) return PSA_OK;
   if (!k || !v || !k_cache || !v_cache || !dev_slots || !aligned16(k) || !aligned16(v) ||
       !aligned16(k_cache) || !aligned16(v_cache) ||
@@ -698,6 +702,13 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
       !(scale > 0.f) || !std::isfinite(scale) || !(logit_cap >= 0.f) ||
       !std::isfinite(logit_cap) || !ok_scales(e4m3_scales))
     return PSA_ERR_INVALID_ARG;
+  if (logit_cap > kChunkMaxCap) return PSA_ERR_UNSUPPORTED;
+  // the factors the kernel works with: the logits' scale in the log2 domain,
+  // with a cap the scale of the exponential in the tanh
+  const float logit_scale = scale * (e4m3_scales ? e4m3_scales->k_scale : 1.f);
+  if (!(logit_scale > 0.f) || !std::isfinite(3.f * logit_scale) ||
+      (logit_cap > 0.f && !std::isfinite(3.f * logit_scale / logit_cap)))
+    return PSA_ERR_INVALID_ARG;
   if (info->n_rows == 0) return PSA_OK;
   // without a page table the key positions are the cache's first rows
   if (!dev_kv_indices && info->n_keys > n_cache_tokens) return PSA_ERR_INVALID_ARG;
@@ -706,6 +717,10 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
       (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(dev_kv_indices) & 3u))
     return PSA_ERR_INVALID_ARG;
+  // a block's rows are read while others are written already
+  const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), o_at = reinterpret_cast<uintptr_t>(o);
+  const uint64_t rows_bytes = uint64_t(T) * info->Hq * info->head_dim * 2;
+  if (q_at < o_at + rows_bytes && o_at < q_at + rows_bytes) return PSA_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < psa_chunk_workspace_size(info) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PSA_ERR_WORKSPACE;

@@ -142,7 +142,7 @@ __device__ __forceinline__ Unit load_unit(const Params& p, const int4* units, in
       x.q0 >= 0 && x.ntok > 0 && x.ntok <= (x.twin ? 1 : 2) * p.TPH &&
           int64_t(x.q0) + x.ntok <= p.n_rows && x.kvh >= 0 && x.kvh < p.Hkv && x.kv0 >= 0 &&
           x.t0 >= 0 && x.t1 > x.t0 && int64_t(x.kv0) + x.t1 <= p.n_keys && x.part >= -1 &&
-          int64_t(x.part) + (x.twin ? 2 : 1) * x.ntok * p.G <= p.part_rows + (x.part < 0),
+          (x.part < 0 || x.part + int64_t(x.twin ? 2 : 1) * x.ntok * p.G <= p.part_rows),
       p.status);
   return x;
 }

@@ -142,7 +142,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
     const int32_t n = qo_lens[b], L = kv_lens[b];
     if (n < 0 || L < n) return PSA_ERR_INVALID_ARG;
     first.push_back(int32_t(blocks.size()));
-    if (q0 + n > INT32_MAX / int64_t(Hq) || kv0 + L > INT32_MAX) return PSA_ERR_INVALID_ARG;
+    if (q0 + n > INT32_MAX / int64_t(Hq) || kv0 + L > INT32_MAX - 2 * kTile) return PSA_ERR_INVALID_ARG;
     for (int32_t i = 0; i < n; i += 2 * tph) {
       Block k;
       k.q0 = int32_t(q0 + i);
@@ -184,7 +184,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
     // whole blocks, then pieces of the mean list's length over `rounds`
     for (double rounds : {0.0, 0.5, 0.75, 1.0, 1.5, 1.75, 2.0, 2.5, 3.0}) {
       const double len = rounds == 0 ? 1e18 : std::max(0.5, total / (double(n_ctas) * rounds));
-      if (rounds > 0 && blocks.size() * double(Hkv) + total / len > 65536.0) break;
+      if (rounds > 0 && blocks.size() * double(Hkv) + total / len > 8192.0) break;
       offer(plan_pieces(blocks, first, Hkv, n_ctas, len));
       if (len <= 0.5) break;
     }

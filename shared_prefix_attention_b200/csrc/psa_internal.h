@@ -190,6 +190,10 @@ int launch_cache_read(const CacheReadArgs& a);
 
 // ---------------------------------------------------------------- chunk
 
+// The largest logit cap: c tanh(s / c) is formed as c - 2 c / (1 + exp(2 s /
+// c)), off by about 2^-22 c, here at most 2.4e-4.
+constexpr float kChunkMaxCap = 1000.f;
+
 struct ChunkArgs {
   const void* q;   // bf16 [n_rows, Hq, D]
   const void* kc;  // bf16 or e4m3 [n_cache, Hkv, D]

@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
     const size_t y0 = size_t(out_row) * p.H[k.kind];
 
     for (int hb = k.h0; hb < k.h1; hb += ROWS) {
-      ok = mbar_wait(ring.bar + ring.got % kDepth, (ring.got / kDepth) & 1, &abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, mbar_wait(ring.bar + ring.got % kDepth,
+                                             (ring.got / kDepth) & 1, &abort_flag, p.status));
       if (!ok) break;
       const T* rows = reinterpret_cast<const T*>(ring.at(ring.got));
 #pragma unroll
@@ -544,7 +545,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
       load_turn<INTER>(turn, p.cos_sin + int64_t(here.at) * p.rot, p.rot, l, -1.f);
     T* d0 = static_cast<T*>(p.y[kind]) + int64_t(t) * p.dxs[kind];
     for (int hb = h0; hb < h1; hb += ROWS) {
-      ok = mbar_wait(ring.bar + ring.got % kDepth, (ring.got / kDepth) & 1, &abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, mbar_wait(ring.bar + ring.got % kDepth,
+                                             (ring.got / kDepth) & 1, &abort_flag, p.status));
       if (!ok) break;
       const T* gr = reinterpret_cast<const T*>(ring.at(ring.got));
       const T* xr = reinterpret_cast<const T*>(ring.at(ring.got) + HALF);

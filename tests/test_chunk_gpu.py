@@ -273,15 +273,17 @@ def test_cache_rows_beyond_32_bit_offsets():
 
 
 def test_debug_build_agrees():
-    """The bounds-checked library on the same calls."""
-    ql, kl, q, k, v, _, _, table, plan = small()
-    want, wl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
-    st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    with psa.use_library(psa.DEBUG_LIB_PATH):
-        got, gl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table, status=st)
-        torch.cuda.synchronize()
-    assert psa.read_status(st) == 0
-    assert torch.equal(got, want) and torch.equal(gl, wl)
+    """The bounds-checked library on the same calls, with and without split
+    blocks."""
+    for kw in (dict(), dict(ql=(3,), kl=(90,)), dict(ql=(9000,), kl=(9000,), Hq=32, Hkv=8)):
+        ql, kl, q, k, v, _, _, table, plan = small(**kw)
+        want, wl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        with psa.use_library(psa.DEBUG_LIB_PATH):
+            got, gl = psa.chunk(q, k, v, plan, 0.1, kv_indices=table, status=st)
+            torch.cuda.synchronize()
+        assert psa.read_status(st) == 0
+        assert torch.equal(got, want) and torch.equal(gl, wl)
 
 
 def test_agrees_with_the_verify_entry():

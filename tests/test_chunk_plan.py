@@ -115,6 +115,7 @@ def test_empty_plans():
     ([1], [4], 8, 2, 256, 0, 148, psa.PSA_ERR_UNSUPPORTED),
     ([1], [4], 129, 1, 128, 0, 148, psa.PSA_ERR_UNSUPPORTED),
     ([1, 1], [2**31 - 1, 2**31 - 1], 8, 2, 128, 0, 148, psa.PSA_ERR_INVALID_ARG),
+    ([1], [2**31 - 100], 8, 2, 128, 0, 148, psa.PSA_ERR_INVALID_ARG),
 ])
 def test_plan_refusals(ql, kl, Hq, Hkv, d, window, n_ctas, status):
     with pytest.raises(psa.PsaError) as e:
@@ -148,7 +149,7 @@ def _info(**kw):
 
 
 def _chunk(**kw):
-    a = dict(q=16, k=16, v=16, ntok=2000, table=None, sc=None, o=32, lse=None, T=300, scale=0.1,
+    a = dict(q=16, k=16, v=16, ntok=2000, table=None, sc=None, o=1 << 30, lse=None, T=300, scale=0.1,
              cap=0.0, info=_info(), plan=16, ws=256, wsb=1 << 40)
     a.update(kw)
     sc = ctypes.byref(psa.KvScales(*a["sc"])) if a["sc"] else None
@@ -161,11 +162,13 @@ def _chunk(**kw):
 def test_chunk_host_validation():
     bad = psa.PSA_ERR_INVALID_ARG
     for kw in (dict(info=None), dict(T=299), dict(ntok=1999), dict(ntok=2**31), dict(scale=0.0),
-               dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")), dict(q=8),
+               dict(scale=float("inf")), dict(scale=3e38), dict(scale=1.0, cap=1e-39), dict(cap=-1.0),
+               dict(o=16), dict(o=16 + 300 * 8 * 128), dict(cap=float("nan")), dict(q=8),
                dict(q=None), dict(k=None), dict(v=24 + 1), dict(o=None), dict(lse=2),
                dict(table=2), dict(plan=None), dict(plan=8), dict(sc=(0.0, 1.0)),
                dict(sc=(1.0, float("inf")))):
         assert _chunk(**kw) == bad, kw
+    assert _chunk(cap=1001.0) == psa.PSA_ERR_UNSUPPORTED
     for kw in (dict(ws=None), dict(ws=128), dict(wsb=255)):
         assert _chunk(**kw) == psa.PSA_ERR_WORKSPACE, kw
     assert _chunk(info=_info(n_rows=0), q=None) == psa.PSA_OK  # nothing to do
@@ -232,12 +235,14 @@ def test_cache_append_host_validation():
     bad = psa.PSA_ERR_INVALID_ARG
     for kw in (dict(T=-1), dict(Hkv=0), dict(Hq=0), dict(ntok=-1), dict(ntok=2**31), dict(k=None),
                dict(v=None), dict(kc=None), dict(vc=8), dict(slots=None), dict(slots=2),
-               dict(ks=255), dict(vs=0), dict(qo=None), dict(sc=(-1.0, 1.0))):
+               dict(ks=255), dict(vs=0), dict(qo=None), dict(sc=(-1.0, 1.0)),
+               dict(sc=(1.0, 1e-39))):
         assert _append(**kw) == bad, kw
     for kw in BAD_HOW:
         assert _append(how=_how(**kw)) == bad, kw
     assert _append(d=80) == psa.PSA_ERR_UNSUPPORTED
     assert _append(T=0) == psa.PSA_OK
+    assert _append(T=0, how=_how(positions=None)) == psa.PSA_OK
 
 
 def _read(**kw):
@@ -281,3 +286,11 @@ def test_binding_refuses_tensors_that_do_not_fit():
         psa.chunk(x, x, x, plan, 1.0)
     with pytest.raises(ValueError):
         psa.build_chunk_plan([1, 2], [3], 2, 2, 128)
+
+
+def test_large_batches_are_planned_quickly():
+    """4096 decoding requests: one plan per step has to stay cheap."""
+    import time
+    t = time.perf_counter()
+    _, info = psa.build_chunk_plan([1] * 4096, [1000 + i % 700 for i in range(4096)], 32, 8, 128)
+    assert info.n_units >= 4096 * 8 and time.perf_counter() - t < 0.5

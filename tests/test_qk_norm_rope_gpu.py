@@ -151,6 +151,12 @@ def test_zero_rows_and_zero_tokens():
     assert yq.shape == (0, 4, 128)
     out = psa.qk_norm_rope_bwd(e, e, e, e, None, None, w, w)
     assert not out[2].any() and not out[3].any()  # sums over nothing
+    cs, none = angles(4, 128, g), torch.empty(0, dtype=torch.int32, device="cuda")
+    assert psa.qk_norm_rope(e, e, none, cs, w, w)[0].shape == (0, 4, 128)
+    c = torch.zeros(3, 4, 128, dtype=torch.bfloat16, device="cuda")
+    assert psa.cache_append(e, e, e, c, c.clone(), none, none, cs, w, w).shape == (0, 4, 128)
+    with pytest.raises(ValueError):
+        psa.qk_norm_rope(q, k, torch.zeros(10, dtype=torch.int32, device="cuda"), cs[:0])
 
 
 def test_bad_position_is_reported_and_skipped():
