@@ -263,10 +263,7 @@ struct RowParams {
   int64_t xs[3];         // their token strides, elements
   void *y[3];            // q_out; k_out or k cache; v cache
   int32_t H[3];          // heads of each kind (0: the kind takes no part)
-  int32_t slices[3];     // warps a token's heads of the kind are split over
-  int32_t hs;            // heads per slice
-  int32_t nslice;        // slices[0] + slices[1] + slices[2]
-  bool whole;            // the warps take whole tokens
+  int32_t stages[3];     // ring stages of a token's heads of the kind
   int32_t T;
   const int32_t* pos;
   const float* cos_sin;
@@ -305,42 +302,53 @@ __device__ __forceinline__ bool place_turns(const RowParams& p, const Place& v, 
   return false;
 }
 
-// One task: heads [h0, h1) of one kind of one token.
+// A warp's share of the work: an equal range of all stages (tokens in order,
+// within a token its kinds), so the warps end together whatever the sizes.
+struct Walk {
+  int t, s;      // token, and stage within it
+  int64_t left;  // stages to go
+  int step;      // to the next token
+};
+__device__ __forceinline__ Walk make_walk(int64_t warp, int64_t warps, int T, int per_token) {
+  const int64_t all = int64_t(T) * per_token, begin = all * warp / warps;
+  Walk w;
+  w.t = int(begin / per_token);
+  w.s = int(begin - int64_t(w.t) * per_token);
+  w.left = all * (warp + 1) / warps - begin;
+  w.step = 1;
+  return w;
+}
+// Or every warps-th token, whole.
+__device__ __forceinline__ Walk make_strided_walk(int64_t warp, int64_t warps, int T,
+                                                  int per_token) {
+  Walk w;
+  w.t = int(warp);
+  w.s = 0;
+  w.left = warp < T ? ((T - 1 - warp) / warps + 1) * per_token : 0;
+  w.step = int(warps);
+  return w;
+}
+// The walk's next task, heads [h0, h1) of one kind of one token, `rows` of
+// them to a stage; the walk moves behind it.
 struct Task {
   int t, kind, h0, h1;
 };
-
-// A warp's walk over its tasks.  With tokens enough for every warp (no heads
-// split, see plan_rows) it takes whole tokens, so that the kinds' sizes even
-// out; otherwise single tasks, whose number then fits 32 bits.
-struct Walk {
-  int64_t i;  // token, or task
-  int s = 0;  // slice of the token
-};
-__device__ __forceinline__ bool walk_ends(const RowParams& p, const Walk& w) {
-  return w.i >= (p.whole ? int64_t(p.T) : int64_t(p.T) * p.nslice);
-}
-__device__ __forceinline__ void walk_on(const RowParams& p, Walk& w, int64_t stride) {
-  if (p.whole && ++w.s < p.nslice) return;
-  w.s = 0;
-  w.i += stride;
-}
-__device__ __forceinline__ Task task_at(const RowParams& p, const Walk& w) {
+__device__ __forceinline__ Task next_task(const RowParams& p, Walk& w, int rows) {
   Task k;
-  int s = w.s;
-  k.t = int(w.i);
-  if (!p.whole) {
-    k.t = int(uint32_t(w.i) / uint32_t(p.nslice));
-    s = int(uint32_t(w.i) - uint32_t(k.t) * uint32_t(p.nslice));
-  }
+  k.t = w.t;
   k.kind = 0;
-  while (k.kind < 2 && s >= p.slices[k.kind]) s -= p.slices[k.kind++];
-  k.h0 = s * p.hs;
-  k.h1 = min(k.h0 + p.hs, p.H[k.kind]);
+  int s = w.s;
+  while (k.kind < 2 && s >= p.stages[k.kind]) s -= p.stages[k.kind++];
+  const int n = int(min(int64_t(p.stages[k.kind] - s), w.left));
+  k.h0 = s * rows;
+  k.h1 = min(k.h0 + n * rows, p.H[k.kind]);
+  w.left -= n;
+  w.s += n;
+  if (w.s == p.stages[0] + p.stages[1] + p.stages[2]) w.s = 0, w.t += w.step;
   return k;
 }
 
-// Forward and append: the warps stride over the tasks.
+// Forward and append.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   constexpr int LPR = D / 16, GROUPS = 32 / LPR;
@@ -351,9 +359,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
-  const int64_t stride = int64_t(gridDim.x) * kRowWarps;
-  Walk walk;
-  walk.i = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  Walk walk = make_walk(int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5),
+                        int64_t(gridDim.x) * kRowWarps, p.T,
+                        p.stages[0] + p.stages[1] + p.stages[2]);
   Ring ring = make_ring(smem, bars);
 
   // the copies run ahead: their own walk over the tasks
@@ -362,10 +370,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   int nh = 0;
   auto put = [&]() {
     if (nh >= n.h1) {
-      if (walk_ends(p, next)) return;
-      n = task_at(p, next);
+      if (next.left == 0) return;
+      n = next_task(p, next, ROWS);
       nh = n.h0;
-      walk_on(p, next, stride);
     }
     if (lane == 0) {
       const T* src = static_cast<const T*>(p.x[n.kind]) + int64_t(n.t) * p.xs[n.kind] +
@@ -383,12 +390,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
 
   bool ok = true;
   Place place = {};
-  if (!walk_ends(p, walk)) place = load_place(p, task_at(p, walk).t);
-  while (ok && !walk_ends(p, walk)) {
-    const Task k = task_at(p, walk);
+  if (walk.left > 0) place = load_place(p, walk.t);
+  while (ok && walk.left > 0) {
+    const Task k = next_task(p, walk, ROWS);
     const Place here = place;
-    walk_on(p, walk, stride);
-    if (!walk_ends(p, walk)) place = load_place(p, task_at(p, walk).t);
+    if (walk.left > 0) place = load_place(p, walk.t);
     // where the rows go: dense by token, or the token's cache row (a padded
     // token caches nothing)
     int64_t out_row = k.t;
@@ -469,8 +475,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   }
 }
 
-// Backward: every block works on one kind and strides over its tasks, so that
-// it sums its rows' weight gradients in registers and writes one partial; the
+// Backward: every block works on one kind, so that it sums its rows' weight gradients in registers and writes one partial; the
 // order of every sum is fixed by the sizes alone.  A stage holds rows of x and
 // of the upstream gradient.
 template <typename T, int D, bool INTER>
@@ -491,29 +496,36 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
   const int blocks = kind ? int(gridDim.x) - p.blocks_q : p.blocks_q;
   const Pieces pc = pieces_of<INTER>(l, p.rot);
   const bool norms = p.w[kind] != nullptr;
-  const int H = p.H[kind], slices = p.slices[kind];
+  const int H = p.H[kind], per_token = p.stages[kind];
   uint64_t w[8], dw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = 0ull;
   if (norms) load_weight(p.w[kind], p.w_dtype, pc, w);
-  const int64_t tasks = int64_t(p.T) * slices;
-  const int64_t stride = int64_t(blocks) * kRowWarps;
-  int64_t task = int64_t(block) * kRowWarps + warp;
+  // With many tokens a warp, the warps side by side read faster than equal
+  // ranges (41 tokens: 289 us against 309); with few, equal ranges end
+  // together (5 tokens: 36.0 us against 37.3).
+  const int64_t warps = int64_t(blocks) * kRowWarps;
+  Walk walk = p.T >= 16 * warps
+                  ? make_strided_walk(int64_t(block) * kRowWarps + warp, warps, p.T, per_token)
+                  : make_walk(int64_t(block) * kRowWarps + warp, warps, p.T, per_token);
   Ring ring = make_ring(smem, bars);
 
-  // (heads are only split where the tasks fit 32 bits, see plan_rows)
-  auto token_of = [&](int64_t i) {
-    return slices == 1 ? int(i) : int(uint32_t(i) / uint32_t(slices));
+  // heads [h0, h1) of a token; the walk moves behind them
+  auto next_rows = [&](Walk& at, int& t, int& h0, int& h1) {
+    const int n = int(min(int64_t(per_token - at.s), at.left));
+    t = at.t;
+    h0 = at.s * ROWS;
+    h1 = min(h0 + n * ROWS, H);
+    at.left -= n;
+    at.s += n;
+    if (at.s == per_token) at.s = 0, at.t += at.step;
   };
-  int64_t next = task;
+  Walk next = walk;
   int nt = 0, nh = 0, nh1 = 0;
   auto put = [&]() {
     if (nh >= nh1) {
-      if (next >= tasks) return;
-      nt = token_of(next);
-      nh = int(next - int64_t(nt) * slices) * p.hs;
-      nh1 = min(nh + p.hs, H);
-      next += stride;
+      if (next.left == 0) return;
+      next_rows(next, nt, nh, nh1);
     }
     if (lane == 0) {
       const uint32_t bytes = uint32_t(min(ROWS, nh1 - nh)) * D * sizeof(T);
@@ -533,12 +545,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
 
   bool ok = true;
   Place place = {};
-  if (task < tasks) place = load_place(p, token_of(task));
-  for (; task < tasks && ok; task += stride) {
-    const int t = token_of(task);
-    const int h0 = int(task - int64_t(t) * slices) * p.hs, h1 = min(h0 + p.hs, H);
+  if (walk.left > 0) place = load_place(p, walk.t);
+  while (ok && walk.left > 0) {
+    int t, h0, h1;
+    next_rows(walk, t, h0, h1);
     const Place here = place;
-    if (task + stride < tasks) place = load_place(p, token_of(task + stride));
+    if (walk.left > 0) place = load_place(p, walk.t);
     const bool live = place_turns(p, here, lane);
     Turn turn;
     if (pc.on && live)
@@ -691,26 +703,6 @@ __global__ void __launch_bounds__(256) cache_read_kernel(
   }
 }
 
-// Heads per task: all of a token's heads of a kind (its angles and weights are
-// loaded once) unless the call has too few tokens to give every SM sixteen
-// warps; then they are split until it has, or until a task is one row group.
-void plan_rows(RowParams& p, int D) {
-  const int groups = 32 / (D / 16);
-  const int64_t want = kRowsBlocks * kRowWarps;
-  const int64_t n = p.T > 0 ? (want + p.T - 1) / p.T : 1;
-  const int hmax = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
-  int64_t hs = (hmax + n - 1) / n;
-  hs = (hs + groups - 1) / groups * groups;
-  if (hs < groups) hs = groups;
-  p.hs = int32_t(hs);
-  p.whole = n == 1;
-  p.nslice = 0;
-  for (int k = 0; k < 3; ++k) {
-    p.slices[k] = (p.H[k] + p.hs - 1) / p.hs;
-    p.nslice += p.slices[k];
-  }
-}
-
 RowParams row_params(const RowsArgs& a) {
   RowParams p = {};
   p.x[0] = a.q, p.x[1] = a.k, p.x[2] = a.v;
@@ -749,12 +741,18 @@ int launch_ring(uint32_t grid, cudaStream_t stream, const RowParams& p) {
   return cudaGetLastError() == cudaSuccess ? PSA_OK : PSA_ERR_CUDA;
 }
 
+// Stages of `rows` heads that a token has in each kind.
+void count_stages(RowParams& p, int rows) {
+  for (int k = 0; k < 3; ++k) p.stages[k] = int32_t((int64_t(p.H[k]) + rows - 1) / rows);
+}
+
 template <typename T, int D>
 int launch_rows_d(const RowsArgs& a) {
   RowParams p = row_params(a);
-  plan_rows(p, D);
-  const int64_t tasks = int64_t(p.T) * p.nslice;
-  int64_t grid = ((p.whole ? int64_t(p.T) : tasks) + kRowWarps - 1) / kRowWarps;
+  count_stages(p, kStageBytes / (D * int(sizeof(T))));
+  // two blocks per SM, or as many as give every warp a stage
+  const int64_t all = int64_t(p.T) * (int64_t(p.stages[0]) + p.stages[1] + p.stages[2]);
+  int64_t grid = (all + kRowWarps - 1) / kRowWarps;
   if (grid > kRowsBlocks) grid = kRowsBlocks;
   return a.how.interleaved ? launch_ring<rows_kernel<T, D, true>>(uint32_t(grid), a.stream, p)
                            : launch_ring<rows_kernel<T, D, false>>(uint32_t(grid), a.stream, p);
@@ -763,14 +761,14 @@ int launch_rows_d(const RowsArgs& a) {
 template <typename T, int D>
 int launch_rows_bwd_d(const RowsBwdArgs& b) {
   RowParams p = row_params(b.rows);
-  plan_rows(p, D);
+  count_stages(p, kStageBytes / 2 / (D * int(sizeof(T))));
   p.dy[0] = b.dq_out, p.dy[1] = b.dk_out;
   p.dxs[0] = b.dq_stride, p.dxs[1] = b.dk_stride;
   p.part = b.part;
   // two blocks per SM in all, shared between the kinds by their rows
   int64_t need[2], blocks[2];
   for (int k = 0; k < 2; ++k)
-    need[k] = (int64_t(p.T) * p.slices[k] + kRowWarps - 1) / kRowWarps;
+    need[k] = (int64_t(p.T) * p.stages[k] + kRowWarps - 1) / kRowWarps;
   const int64_t H = int64_t(p.H[0]) + p.H[1];
   for (int k = 0; k < 2; ++k) {
     const int64_t share = H ? (kRowsBlocks * int64_t(p.H[k]) + H - 1) / H : 0;
