@@ -258,12 +258,22 @@ __device__ __forceinline__ float dot16(const uint64_t (&a)[8], const uint64_t (&
   return pair_sum(f2_add(s0, s1));
 }
 
+// What each of a launch's warps takes: `stages` ring stages, and `more` of the
+// warps, spread among them, one more.  (A stage is at least 128 bytes of its
+// own memory, so that 32 bits hold the number of all.  With the first `more`
+// warps taking it, the warps' rows lie one fixed step apart: 49152 tokens 182
+// us against 172.)
+struct Share {
+  int32_t stages, more, warps;
+};
+
 struct RowParams {
   const void *x[3];      // q, k, v rows in
   int64_t xs[3];         // their token strides, elements
   void *y[3];            // q_out; k_out or k cache; v cache
   int32_t H[3];          // heads of each kind (0: the kind takes no part)
   int32_t stages[3];     // ring stages of a token's heads of the kind
+  Share share[2];        // of all kinds; the backward: of q, of k
   int32_t T;
   const int32_t* pos;
   const float* cos_sin;
@@ -304,28 +314,29 @@ __device__ __forceinline__ bool place_turns(const RowParams& p, const Place& v, 
 
 // A warp's share of the work: an equal range of all stages (tokens in order,
 // within a token its kinds), so the warps end together whatever the sizes.
+// The host divides (Share).
 struct Walk {
-  int t, s;      // token, and stage within it
-  int64_t left;  // stages to go
-  int step;      // to the next token
+  int t, s;  // token, and stage within it
+  int left;  // stages to go
+  int step;  // to the next token
 };
-__device__ __forceinline__ Walk make_walk(int64_t warp, int64_t warps, int T, int per_token) {
-  const int64_t all = int64_t(T) * per_token, begin = all * warp / warps;
+__device__ __forceinline__ Walk make_walk(int warp, const Share& share, int per_token) {
+  auto extra = [&](int w) { return int(uint32_t(w) * share.more / uint32_t(share.warps)); };
+  const int begin = warp * share.stages + extra(warp);
   Walk w;
-  w.t = int(begin / per_token);
-  w.s = int(begin - int64_t(w.t) * per_token);
-  w.left = all * (warp + 1) / warps - begin;
+  w.t = int(uint32_t(begin) / uint32_t(per_token));
+  w.s = begin - w.t * per_token;
+  w.left = share.stages + extra(warp + 1) - extra(warp);
   w.step = 1;
   return w;
 }
 // Or every warps-th token, whole.
-__device__ __forceinline__ Walk make_strided_walk(int64_t warp, int64_t warps, int T,
-                                                  int per_token) {
+__device__ __forceinline__ Walk make_strided_walk(int warp, int warps, int T, int per_token) {
   Walk w;
-  w.t = int(warp);
+  w.t = warp;
   w.s = 0;
   w.left = warp < T ? ((T - 1 - warp) / warps + 1) * per_token : 0;
-  w.step = int(warps);
+  w.step = warps;
   return w;
 }
 // The walk's next task, heads [h0, h1) of one kind of one token, `rows` of
@@ -339,7 +350,7 @@ __device__ __forceinline__ Task next_task(const RowParams& p, Walk& w, int rows)
   k.kind = 0;
   int s = w.s;
   while (k.kind < 2 && s >= p.stages[k.kind]) s -= p.stages[k.kind++];
-  const int n = int(min(int64_t(p.stages[k.kind] - s), w.left));
+  const int n = min(p.stages[k.kind] - s, w.left);
   k.h0 = s * rows;
   k.h1 = min(k.h0 + n * rows, p.H[k.kind]);
   w.left -= n;
@@ -359,8 +370,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
-  Walk walk = make_walk(int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5),
-                        int64_t(gridDim.x) * kRowWarps, p.T,
+  Walk walk = make_walk(int(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), p.share[0],
                         p.stages[0] + p.stages[1] + p.stages[2]);
   Ring ring = make_ring(smem, bars);
 
@@ -475,10 +485,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(RowParams p) {
   }
 }
 
-// Backward: every block works on one kind, so that it sums its rows' weight gradients in registers and writes one partial; the
-// order of every sum is fixed by the sizes alone.  A stage holds rows of x and
-// of the upstream gradient.
-template <typename T, int D, bool INTER>
+// Backward: every block works on one kind, so that it sums its rows' weight
+// gradients in registers and writes one partial; the order of every sum is
+// fixed by the sizes alone.  A stage holds rows of x and of the upstream
+// gradient.  WHOLE: a warp takes every so many-th token, whole.  Side by side
+// the warps read faster than in ranges (49152 tokens of 40 heads: 291 us
+// against 309), but with few tokens each the last round is half empty (6144
+// tokens of 32 heads: 37.4 us against 35.9 in equal ranges).
+template <typename T, int D, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
   constexpr int LPR = D / 16, GROUPS = 32 / LPR;
   constexpr int HALF = kStageBytes / 2;
@@ -501,19 +515,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = 0ull;
   if (norms) load_weight(p.w[kind], p.w_dtype, pc, w);
-  // With many tokens a warp, the warps side by side read faster than equal
-  // ranges (41 tokens: 289 us against 309); with few, equal ranges end
-  // together (5 tokens: 36.0 us against 37.3).
-  const int64_t warps = int64_t(blocks) * kRowWarps;
-  Walk walk = p.T >= 16 * warps
-                  ? make_strided_walk(int64_t(block) * kRowWarps + warp, warps, p.T, per_token)
-                  : make_walk(int64_t(block) * kRowWarps + warp, warps, p.T, per_token);
+  const int warps = blocks * kRowWarps;
+  Walk walk = WHOLE
+                  ? make_strided_walk(block * kRowWarps + warp, warps, p.T, per_token)
+                  : make_walk(block * kRowWarps + warp, p.share[kind], per_token);
   Ring ring = make_ring(smem, bars);
 
   // heads [h0, h1) of a token; the walk moves behind them
   auto next_rows = [&](Walk& at, int& t, int& h0, int& h1) {
-    const int n = int(min(int64_t(per_token - at.s), at.left));
     t = at.t;
+    if (WHOLE) {
+      h0 = 0;
+      h1 = H;
+      at.left -= per_token;
+      at.t += at.step;
+      return;
+    }
+    const int n = min(per_token - at.s, at.left);
     h0 = at.s * ROWS;
     h1 = min(h0 + n * ROWS, H);
     at.left -= n;
@@ -746,6 +764,13 @@ void count_stages(RowParams& p, int rows) {
   for (int k = 0; k < 3; ++k) p.stages[k] = int32_t((int64_t(p.H[k]) + rows - 1) / rows);
 }
 
+// `blocks` blocks' warps over n stages.
+Share share_of(int64_t n, int64_t blocks) {
+  const int64_t warps = blocks * kRowWarps;
+  if (warps == 0) return {};
+  return {int32_t(n / warps), int32_t(n % warps), int32_t(warps)};
+}
+
 template <typename T, int D>
 int launch_rows_d(const RowsArgs& a) {
   RowParams p = row_params(a);
@@ -753,7 +778,9 @@ int launch_rows_d(const RowsArgs& a) {
   // two blocks per SM, or as many as give every warp a stage
   const int64_t all = int64_t(p.T) * (int64_t(p.stages[0]) + p.stages[1] + p.stages[2]);
   int64_t grid = (all + kRowWarps - 1) / kRowWarps;
+  if (all > INT32_MAX) return PSA_ERR_INVALID_ARG;
   if (grid > kRowsBlocks) grid = kRowsBlocks;
+  p.share[0] = share_of(all, grid);
   return a.how.interleaved ? launch_ring<rows_kernel<T, D, true>>(uint32_t(grid), a.stream, p)
                            : launch_ring<rows_kernel<T, D, false>>(uint32_t(grid), a.stream, p);
 }
@@ -767,8 +794,10 @@ int launch_rows_bwd_d(const RowsBwdArgs& b) {
   p.part = b.part;
   // two blocks per SM in all, shared between the kinds by their rows
   int64_t need[2], blocks[2];
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 2; ++k) {
+    if (int64_t(p.T) * p.stages[k] > INT32_MAX) return PSA_ERR_INVALID_ARG;
     need[k] = (int64_t(p.T) * p.stages[k] + kRowWarps - 1) / kRowWarps;
+  }
   const int64_t H = int64_t(p.H[0]) + p.H[1];
   for (int k = 0; k < 2; ++k) {
     const int64_t share = H ? (kRowsBlocks * int64_t(p.H[k]) + H - 1) / H : 0;
@@ -776,11 +805,17 @@ int launch_rows_bwd_d(const RowsBwdArgs& b) {
   }
   if (blocks[0] + blocks[1] > kRowsBlocks) --blocks[blocks[0] > blocks[1] ? 0 : 1];
   p.blocks_q = int32_t(blocks[0]);
+  for (int k = 0; k < 2; ++k) p.share[k] = share_of(int64_t(p.T) * p.stages[k], blocks[k]);
   const uint32_t grid = uint32_t(blocks[0] + blocks[1]);
   if (grid > 0) {  // without tokens the weight gradients are zero
-    const int rc = b.rows.how.interleaved
-                       ? launch_ring<rows_bwd_kernel<T, D, true>>(grid, b.rows.stream, p)
-                       : launch_ring<rows_bwd_kernel<T, D, false>>(grid, b.rows.stream, p);
+    // sixteen tokens for every warp: the last round costs a few percent at most
+    const bool whole = p.T >= 16 * int64_t(grid) * kRowWarps;
+    const int rc =
+        b.rows.how.interleaved
+            ? (whole ? launch_ring<rows_bwd_kernel<T, D, true, true>>(grid, b.rows.stream, p)
+                     : launch_ring<rows_bwd_kernel<T, D, true, false>>(grid, b.rows.stream, p))
+            : (whole ? launch_ring<rows_bwd_kernel<T, D, false, true>>(grid, b.rows.stream, p)
+                     : launch_ring<rows_bwd_kernel<T, D, false, false>>(grid, b.rows.stream, p));
     if (rc != PSA_OK) return rc;
   }
   if (!b.dq_weight && !b.dk_weight) return PSA_OK;

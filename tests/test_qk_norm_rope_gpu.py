@@ -231,6 +231,12 @@ def test_backward(T, Hq, Hkv, d, rot, inter, dtype, wdt, strided):
         assert torch.equal(a, b)  # a fixed order of every sum
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,inter", [(9, 1, 128, False), (2, 3, 64, True)])
+def test_backward_of_many_tokens(Hq, Hkv, d, inter):
+    """Enough tokens that every warp takes whole ones."""
+    test_backward(40001, Hq, Hkv, d, d, inter, torch.bfloat16, torch.float32, True)
+
+
 def test_backward_against_differences():
     """Central differences of the forward kernel itself, fp32: a step h moves
     <y, dy> by h dx + O(h^3); with |values| ~ 1 and sums of 2 * 64 terms the
