@@ -19,18 +19,21 @@ constexpr int kTile = psa::kChunkTile;
 
 // Costs in units of one 128-key tile of a full block (both 128-row halves).
 // A block whose rows fit one half runs "twin": the halves take alternate
-// tiles of the same rows, so a tile costs less (the loaders set its pace).  A piece pays
-// for its first tile's latency and its epilogue, a split block for its
-// partial rows and the join launch.
-constexpr double kTwinTile = 0.8, kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
+// tiles of the same rows, so a tile costs less: the loaders set its pace, and
+// 64-wide heads give them half the bytes (3 x 777 tokens of 16 such heads,
+// capped: 132 us at 0.7 against 138 at 0.8; uncapped 74.5 / 76.8, and 79.8 at
+// 0.6).  A piece pays for its first tile's latency and its epilogue, a split
+// block for its partial rows and the join launch.
+constexpr double kTwinTile = 0.8, kTwinTile64 = 0.7;
+constexpr double kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
 
 struct Block {
   int32_t q0, ntok, pos0, kv0, lo, hi;  // keys [lo, hi) are seen by some row
   bool twin;
+  double tile_cost;
   int32_t tiles() const { return int32_t((int64_t(hi) - lo + kTile - 1) / kTile); }
-  double tile_cost() const { return twin ? kTwinTile : 1.0; }
   double cost(int32_t n) const {  // of a piece of n tiles
-    return n * tile_cost() + kPieceCost + (n < tiles() || (twin && n > 1) ? kSplitCost : 0.0);
+    return n * tile_cost + kPieceCost + (n < tiles() || (twin && n > 1) ? kSplitCost : 0.0);
   }
 };
 
@@ -53,7 +56,7 @@ Plan plan_pieces(const std::vector<Block>& blocks, const std::vector<int32_t>& f
                  int32_t n_ctas, double len) {
   Plan plan;
   auto count = [&](const Block& b) {
-    const int32_t per = int32_t(std::min(1e9, std::max(1.0, len / b.tile_cost())));
+    const int32_t per = int32_t(std::min(1e9, std::max(1.0, len / b.tile_cost)));
     return (b.tiles() + per - 1) / per;
   };
   // the KV heads are alike: list and sort one head's pieces, then repeat them
@@ -113,7 +116,7 @@ bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, d
           int32_t fit = n - t;
           if (load + k.cost(fit) > budget) {
             const double left = budget - load - kPieceCost - kSplitCost;
-            fit = std::min(n - t, int32_t(left / k.tile_cost()));
+            fit = std::min(n - t, int32_t(left / k.tile_cost));
             // no stubs: a cut leaves at least two tiles on both sides
             if (n - t - fit < 2) fit = n - t - 2;
             if (fit < 2) {
@@ -152,6 +155,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
       k.lo = window > 0 ? std::max(0, k.pos0 - window + 1) : 0;
       k.hi = k.pos0 + k.ntok;
       k.twin = k.ntok <= tph;
+      k.tile_cost = !k.twin ? 1.0 : head_dim == 64 ? kTwinTile64 : kTwinTile;
       blocks.push_back(k);
     }
     q0 += n;
@@ -160,7 +164,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
   first.push_back(int32_t(blocks.size()));
 
   double total = 0.0;
-  for (const Block& k : blocks) total += k.tiles() * k.tile_cost() * Hkv;
+  for (const Block& k : blocks) total += k.tiles() * k.tile_cost * Hkv;
   // a join reads its partials at memory speed, spread over the CTAs
   auto join_cost = [&](const Plan& plan) {
     double rows = 0.0;
