@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(threads<WIDE>(), 1)
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
+  let_next_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ChunkPlanView view(p.n_ctas, p.n_units, p.n_joins);
   if (__ldg(p.plan) != kChunkMagic || __ldg(p.plan + 1) != p.n_ctas ||
@@ -940,12 +941,17 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
   constexpr int PITCH = D * 2 + 16;
   __shared__ __align__(16) uint8_t out[32 * PITCH];
   const ChunkPlanView view(p.n_ctas, p.n_units, p.n_joins);
-  if (__ldg(p.plan) != kChunkMagic || __ldg(p.plan + 1) != p.n_ctas ||
-      __ldg(p.plan + 2) != p.n_units || __ldg(p.plan + 3) != p.n_joins)
-    return;  // reported by the chunk kernel
+  const bool fits = __ldg(p.plan) == kChunkMagic && __ldg(p.plan + 1) == p.n_ctas &&
+                    __ldg(p.plan + 2) == p.n_units && __ldg(p.plan + 3) == p.n_joins;
   const int4* join = reinterpret_cast<const int4*>(p.plan + view.joins + 8 * blockIdx.x);
-  const int4 a = __ldg(join);
-  const int count = __ldg(reinterpret_cast<const int32_t*>(join + 1));
+  int4 a = {};
+  int count = 0;
+  if (fits) {
+    a = __ldg(join);
+    count = __ldg(reinterpret_cast<const int32_t*>(join + 1));
+  }
+  wait_for_previous();
+  if (!fits) return;  // reported by the chunk kernel
   const int q0 = a.x, rows = a.y, kvh = a.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = blockIdx.y * 32;
   if (row0 >= rows) return;
@@ -956,19 +962,13 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
     return;
   const int r = min(row0 + lane, rows - 1);
   const float* lse = p.part_lse + a.w + r;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < count; ++i) m = fmaxf(m, __ldg(lse + size_t(i) * rows));
-  float4 acc[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
   const float4* o0 =
       reinterpret_cast<const float4*>(p.part_o + size_t(a.w) * D) + size_t(warp) * rows + r;
-  // four partials at a time, their loads together
-  for (int i0 = 0; i0 < count; i0 += 4) {
-    float l[4];
-    float4 v[4][N];
+  // Four partials at a time, their loads together; the first four go out
+  // ahead of the maximum over all.
+  float l[4];
+  float4 v[4][N];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       l[j] = -INFINITY;
@@ -979,6 +979,17 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Params p) {
         for (int n = 0; n < N; ++n) v[j][n] = __ldg(src + size_t(n) * 8 * rows);
       }
     }
+  };
+  load(0);
+  float m = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+#pragma unroll 8
+  for (int i = 4; i < count; ++i) m = fmaxf(m, __ldg(lse + size_t(i) * rows));
+  float4 acc[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int i0 = 0; i0 < count; i0 += 4) {
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // an empty partial's rows were not written: whatever they hold stays out
@@ -1084,8 +1095,8 @@ int launch_chunk_d(const ChunkArgs& a) {
   if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
   if (a.info.n_joins > 0) {
     const dim3 grid(a.info.n_joins, (a.info.max_join_rows + 31) / 32);
-    chunk_join_kernel<D><<<grid, 256, 0, a.stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PSA_ERR_CUDA;
+    if (launch_behind(chunk_join_kernel<D>, grid, 256, a.stream, p) != cudaSuccess)
+      return PSA_ERR_CUDA;
   }
   return PSA_OK;
 }

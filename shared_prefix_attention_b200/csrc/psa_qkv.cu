@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
   // at least one row group; fp32 rows of 16 lanes fill the stage with less
   constexpr int ROWS = HALF / (D * int(sizeof(T)));
   extern __shared__ __align__(128) uint8_t smem[];
+  let_next_launch();
   __shared__ float red[kRowWarps][D];
   __shared__ uint64_t bars[kRowWarps][kDepth];
   __shared__ int abort_flag;
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(256) weight_sum_kernel(const float* part, int 
   const int kind = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
   const int b0 = kind ? blocks_q : 0, b1 = kind ? blocks : blocks_q;
   float v = 0.f;
+  wait_for_previous();
 #pragma unroll 4
   for (int b = b0 + j; b < b1; b += 8) v += part[size_t(b) * D + c];
   red[j][threadIdx.x & 31] = v;
@@ -819,9 +821,11 @@ int launch_rows_bwd_d(const RowsBwdArgs& b) {
     if (rc != PSA_OK) return rc;
   }
   if (!b.dq_weight && !b.dk_weight) return PSA_OK;
-  weight_sum_kernel<<<dim3(D / 32, 2), 256, 0, b.rows.stream>>>(
-      b.part, p.blocks_q, int(grid), D, b.dq_weight, b.dk_weight);
-  return cudaGetLastError() == cudaSuccess ? PSA_OK : PSA_ERR_CUDA;
+  return launch_behind(weight_sum_kernel, dim3(D / 32, 2), 256, b.rows.stream,
+                       static_cast<const float*>(b.part), int(p.blocks_q), int(grid), D,
+                       b.dq_weight, b.dk_weight) == cudaSuccess
+             ? PSA_OK
+             : PSA_ERR_CUDA;
 }
 
 }  // namespace
