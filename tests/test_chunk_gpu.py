@@ -254,6 +254,42 @@ def test_two_graphs_and_an_eager_call_at_once():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_layers_in_a_row_share_a_workspace(captured):
+    """Eight calls, each one's queries the output of the one before, all over
+    one workspace whose partials each call's join reads: nothing of a call may
+    begin before the call before it is done."""
+    ql, kl, q, k, v, _, _, table, plan = small(seed=7, ql=(300, 1, 64), kl=(4000, 900, 64))
+    assert plan.info.n_joins > 0
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+
+    def layers():
+        x, every = q, []
+        for i in range(8):
+            x, l = psa.chunk(x, k, v, plan, 0.3 + 0.1 * i, kv_indices=table, workspace=ws)
+            every += [x, l]
+        return every
+
+    if captured:
+        layers()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = layers()
+        ws.fill_(0xff)
+        for _ in range(3):
+            g.replay()
+    else:
+        got = layers()
+    x = q
+    for i in range(8):
+        torch.cuda.synchronize()
+        want = psa.chunk(x, k, v, plan, 0.3 + 0.1 * i, kv_indices=table)
+        torch.cuda.synchronize()
+        assert torch.equal(got[2 * i], want[0]) and torch.equal(got[2 * i + 1], want[1])
+        x = want[0]
+
+
 def test_cache_rows_beyond_32_bit_offsets():
     """Rows whose byte offsets pass 2^32: appended, attended, read back."""
     Hq, Hkv, d, n = 4, 2, 128, 130

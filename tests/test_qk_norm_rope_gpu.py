@@ -237,6 +237,38 @@ def test_backward_of_many_tokens(Hq, Hkv, d, inter):
     test_backward(40001, Hq, Hkv, d, d, inter, torch.bfloat16, torch.float32, True)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_backwards_in_a_row_share_a_workspace(captured):
+    """The sum over a call's partial weight gradients against the next call,
+    which writes its own partials to the same place."""
+    calls = []
+    ws = torch.empty(296 * 128 * 4, dtype=torch.uint8, device="cuda")
+    for i in range(6):
+        g, q, k, _ = make(700, 8, 2, 128, torch.bfloat16, 100 + i)
+        calls.append((q, k, torch.randn_like(q.contiguous()), torch.randn_like(k.contiguous()),
+                      torch.arange(700, device="cuda").int(), angles(700, 128, g),
+                      weight(g, 128), weight(g, 128)))
+
+    def run():
+        return [psa.qk_norm_rope_bwd(*c, EPS, False, workspace=ws) for c in calls]
+
+    if captured:
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run()
+        ws.fill_(0xff)
+        for _ in range(3):
+            graph.replay()
+    else:
+        got = run()
+    for c, a in zip(calls, got):
+        torch.cuda.synchronize()
+        for x, y in zip(a, psa.qk_norm_rope_bwd(*c, EPS, False)):
+            assert torch.equal(x, y)
+
+
 def test_backward_against_differences():
     """Central differences of the forward kernel itself, fp32: a step h moves
     <y, dy> by h dx + O(h^3); with |values| ~ 1 and sums of 2 * 64 terms the
