@@ -494,8 +494,9 @@ typedef struct psa_norm_rope {
  *             are dense, tokens are q_stride / k_stride elements apart (so
  *             both can be slices of one projection's output).  Strides are
  *             multiples of 16 bytes.  Either may be NULL (with its output).
- *   q_out, k_out  device, dense, same dtype (written; may not overlap the
- *             inputs unless they are the same dense tensor)
+ *   q_out, k_out  device, dense, same dtype (written; PSA_ERR_INVALID_ARG if
+ *             one overlaps an input, unless it is that same dense tensor, or
+ *             the other)
  * d in {64, 128, 256}.  A position outside [0, n_positions) sets
  * PSA_ERR_INVALID_ARG in dev_status and its token's rows are not written.
  */
@@ -515,7 +516,9 @@ size_t psa_qk_norm_rope_bwd_workspace_size(int32_t head_dim);
  * norm was applied).
  *   dq_out, dk_out  device dense [T, Hq, d] / [T, Hkv, d]: upstream gradients
  *   dq, dk          device, token strides dq_stride / dk_stride elements
- *                   (written; may be slices of one gradient tensor)
+ *                   (written; may be slices of one gradient tensor, or lie
+ *                   exactly over dq_out or q, dk_out or k; PSA_ERR_INVALID_ARG
+ *                   for any other overlap with an input or each other)
  *   dq_weight, dk_weight  device [d] fp32 (written, not added to; nullable)
  * The order of every sum depends on the sizes alone, so results repeat.
  * A token whose position is outside the table is left out, as above.
@@ -541,8 +544,10 @@ int psa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t
  *             and its position has to be in the table all the same).
  *             A row >= n_cache_tokens sets PSA_ERR_INVALID_ARG in dev_status
  *             and is skipped.  Two tokens with one row race: that row is void.
- *   q_out     device bf16 dense [T, Hq, d] (written)
+ *   q_out     device bf16 dense [T, Hq, d] (written; may be q itself)
  * d in {64, 128, 256}.  Cache rows that no slot names are left as they were.
+ * The caches overlap neither each other nor q, k, v, q_out
+ * (PSA_ERR_INVALID_ARG).
  */
 int psa_cache_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv,
@@ -556,7 +561,8 @@ int psa_cache_append(const void *q, int64_t q_stride, const void *k, int64_t k_s
  * for an e4m3 cache), v alike.
  *   dev_rows  device int32 [n] (a slice of a page table); a row outside the
  *             cache gives zeros and sets PSA_ERR_INVALID_ARG in dev_status
- *   k, v      device bf16 [n, Hkv, d] (written)
+ *   k, v      device bf16 [n, Hkv, d] (written; PSA_ERR_INVALID_ARG if they
+ *             overlap a cache or each other)
  * d in {64, 128, 256}.
  */
 int psa_cache_read(const void *k_cache, const void *v_cache, int64_t n_cache_tokens,
@@ -588,8 +594,8 @@ typedef struct psa_chunk_info {
  * The query rows of a KV head (tokens x the query heads of its group) are cut
  * into blocks of 2 * floor(128 / (Hq / Hkv)) tokens, each block's keys into
  * pieces, and the pieces are handed to n_ctas lists (n_ctas: the CTAs that
- * run at once, one per SM) so that the longest list is as short as a greedy
- * longest-first assignment makes it.  window > 0: a token sees its last
+ * run at once, one per SM): equal pieces longest first, or lists filled one
+ * after another, whichever is expected to end earlier.  window > 0: a token sees its last
  * `window` keys only (itself included); 0: all.
  * out: the plan, to be copied to 16-byte aligned device memory; PSA_ERR_CAPACITY (with
  * info->len set) if cap is smaller.  PSA_ERR_INVALID_ARG for a negative length,
@@ -615,7 +621,8 @@ size_t psa_chunk_workspace_size(const psa_chunk_info *info);
  *   logit_cap  0: none; c > 0: logits become c tanh(logit / c) before the mask
  *              (c <= 1000, PSA_ERR_UNSUPPORTED above: the cap is formed with an
  *              error of about 2^-22 c)
- *   o          device [T, Hq, d] bf16 (written up to n_rows; may not overlap q)
+ *   o          device [T, Hq, d] bf16 (written up to n_rows; PSA_ERR_INVALID_ARG if
+ *              it overlaps q or a cache)
  *   lse        device [T, Hq] fp32 (written up to n_rows; nullable)
  * Token i of request b is at position kv_lens[b] - qo_lens[b] + i and sees the
  * keys up to its own position, the last `window` of them if the plan has a

@@ -658,7 +658,8 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     positions: device int32 [T]; cos_sin: device fp32 [n_positions, rot_dim],
     rot_dim/2 cosines then rot_dim/2 sines of every position (None: no
     rotation).  Pairs are (i, i + rot_dim/2), or (2i, 2i + 1) with
-    ``interleaved``; elements behind rot_dim pass through."""
+    ``interleaved``; elements behind rot_dim pass through.  q_out and k_out may
+    be q and k themselves (dense ones); other overlaps are refused."""
     _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
     dev = q.device
     T, Hq, d, qs = _rows(q, q.dtype, dev, "q")
@@ -681,7 +682,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_
     """Gradients of :func:`qk_norm_rope` for the upstream gradients dq_out and
     dk_out of its outputs: (dq, dk, dq_weight, dk_weight), the weights' in fp32
     and None where there is no weight.  dq and dk may be given as slices of
-    one gradient tensor (dense heads, any token stride of whole 16 bytes)."""
+    one gradient tensor (dense heads, any token stride of whole 16 bytes), or
+    be the upstream gradients or the inputs themselves."""
     _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
     dev = q.device
     T, Hq, d, qs = _rows(q, q.dtype, dev, "q")

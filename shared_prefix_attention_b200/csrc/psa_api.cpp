@@ -534,6 +534,28 @@ bool ok_how(const psa_norm_rope* how, int32_t d, int32_t T) {
   return true;
 }
 
+// T rows of `width` bytes, `pitch` bytes apart.
+struct RowsAt {
+  const void* at;
+  int64_t pitch, width, T;
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(at); }
+  uintptr_t end() const { return begin() + uintptr_t((T - 1) * pitch + width); }
+};
+RowsAt rows_at(const void* at, int64_t stride, int32_t H, int32_t d, int elem, int64_t T) {
+  return {at, stride * elem, int64_t(H) * d * elem, T};
+}
+// Whether writing `out` leaves `in` alone: they share no byte (slices of one
+// tensor lie between each other's rows), or, with `over`, each row is written
+// exactly over itself (the warp that writes it has read it).
+bool apart(const RowsAt& out, const RowsAt& in, bool over) {
+  if (!out.at || !in.at || out.end() <= in.begin() || in.end() <= out.begin()) return true;
+  if (out.at == in.at && out.width == in.width && (out.T == 1 || out.pitch == in.pitch)) return over;
+  if (out.pitch != in.pitch || out.T == 1) return false;
+  int64_t ahead = int64_t(in.begin() - out.begin()) % out.pitch;
+  if (ahead < 0) ahead += out.pitch;
+  return ahead >= out.width && ahead + in.width <= out.pitch;
+}
+
 bool ok_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
 }  // namespace
@@ -554,6 +576,14 @@ extern "C" int psa_qk_norm_rope_fwd(const void* q, int64_t q_stride, const void*
              !ok_stride(q_stride, Hq, head_dim, elem))) ||
       (k && (!k_out || !aligned16(k) || !aligned16(k_out) ||
              !ok_stride(k_stride, Hkv, head_dim, elem))))
+    return PSA_ERR_INVALID_ARG;
+  const RowsAt in_q = rows_at(q, q_stride, Hq, head_dim, elem, T);
+  const RowsAt in_k = rows_at(k, k_stride, Hkv, head_dim, elem, T);
+  const RowsAt out_q = rows_at(q ? q_out : nullptr, int64_t(Hq) * head_dim, Hq, head_dim, elem, T);
+  const RowsAt out_k =
+      rows_at(k ? k_out : nullptr, int64_t(Hkv) * head_dim, Hkv, head_dim, elem, T);
+  if (!apart(out_q, in_q, true) || !apart(out_k, in_k, true) || !apart(out_q, in_k, false) ||
+      !apart(out_k, in_q, false) || !apart(out_q, out_k, false))
     return PSA_ERR_INVALID_ARG;
   RowsArgs a = {};
   a.q = q, a.k = k;
@@ -600,6 +630,22 @@ extern "C" int psa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void*
   if (!workspace || ws_bytes < psa_qk_norm_rope_bwd_workspace_size(head_dim) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PSA_ERR_WORKSPACE;
+  if (T > 0) {
+    // q and k are only read where there is a norm
+    const RowsAt in[2] = {
+        rows_at(how->q_weight ? q : nullptr, q_stride, Hq, head_dim, elem, T),
+        rows_at(how->k_weight ? k : nullptr, k_stride, Hkv, head_dim, elem, T)};
+    const RowsAt up[2] = {
+        rows_at(q ? dq_out : nullptr, int64_t(Hq) * head_dim, Hq, head_dim, elem, T),
+        rows_at(k ? dk_out : nullptr, int64_t(Hkv) * head_dim, Hkv, head_dim, elem, T)};
+    const RowsAt out[2] = {rows_at(q ? dq : nullptr, dq_stride, Hq, head_dim, elem, T),
+                           rows_at(k ? dk : nullptr, dk_stride, Hkv, head_dim, elem, T)};
+    for (int o = 0; o < 2; ++o)
+      for (int i = 0; i < 2; ++i)
+        if (!apart(out[o], in[i], o == i) || !apart(out[o], up[i], o == i))
+          return PSA_ERR_INVALID_ARG;
+    if (!apart(out[0], out[1], false)) return PSA_ERR_INVALID_ARG;
+  }
   RowsBwdArgs b = {};
   b.rows.q = q, b.rows.k = k;
   b.rows.q_stride = q_stride, b.rows.k_stride = k_stride;
@@ -639,6 +685,18 @@ extern "C" int psa_cache_append(const void* q, int64_t q_stride, const void* k, 
       (q && (!q_out || !aligned16(q) || !aligned16(q_out) ||
              !ok_stride(q_stride, Hq, head_dim, 2))))
     return PSA_ERR_INVALID_ARG;
+  const RowsAt in[3] = {rows_at(k, k_stride, Hkv, head_dim, 2, T),
+                        rows_at(v, v_stride, Hkv, head_dim, 2, T),
+                        rows_at(q, q_stride, Hq, head_dim, 2, T)};
+  const RowsAt out = rows_at(q ? q_out : nullptr, int64_t(Hq) * head_dim, Hq, head_dim, 2, T);
+  const int64_t row = int64_t(Hkv) * head_dim * (e4m3_scales ? 1 : 2);
+  const RowsAt kc = {n_cache_tokens ? k_cache : nullptr, row, row, n_cache_tokens};
+  const RowsAt vc = {n_cache_tokens ? v_cache : nullptr, row, row, n_cache_tokens};
+  for (const RowsAt& x : in)
+    if (!apart(out, x, &x == in + 2) || !apart(kc, x, false) || !apart(vc, x, false))
+      return PSA_ERR_INVALID_ARG;
+  if (!apart(kc, out, false) || !apart(vc, out, false) || !apart(kc, vc, false))
+    return PSA_ERR_INVALID_ARG;
   RowsArgs a = {};
   a.q = q, a.k = k, a.v = v;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
@@ -668,6 +726,14 @@ extern "C" int psa_cache_read(const void* k_cache, const void* v_cache, int64_t 
       !aligned16(v_cache) || !aligned16(k) || !aligned16(v) ||
       (reinterpret_cast<uintptr_t>(dev_rows) & 3u))
     return PSA_ERR_INVALID_ARG;
+  const int64_t row = int64_t(Hkv) * head_dim * (e4m3_scales ? 1 : 2);
+  const int64_t dense = int64_t(Hkv) * head_dim * 2;
+  const RowsAt out[2] = {{k, dense, dense, n}, {v, dense, dense, n}};
+  for (const void* c : {k_cache, v_cache})
+    for (const RowsAt& o : out)
+      if (n_cache_tokens && !apart(o, {c, row, row, n_cache_tokens}, false))
+        return PSA_ERR_INVALID_ARG;
+  if (!apart(out[0], out[1], false)) return PSA_ERR_INVALID_ARG;
   CacheReadArgs a = {};
   a.kc = k_cache, a.vc = v_cache;
   a.n_cache = n_cache_tokens;
@@ -721,6 +787,11 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
   const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), o_at = reinterpret_cast<uintptr_t>(o);
   const uint64_t rows_bytes = uint64_t(T) * info->Hq * info->head_dim * 2;
   if (q_at < o_at + rows_bytes && o_at < q_at + rows_bytes) return PSA_ERR_INVALID_ARG;
+  const int64_t row = int64_t(info->Hkv) * info->head_dim * (e4m3_scales ? 1 : 2);
+  for (const void* c : {k_cache, v_cache})
+    if (n_cache_tokens && !apart({o, int64_t(rows_bytes), int64_t(rows_bytes), 1},
+                                 {c, row, row, n_cache_tokens}, false))
+      return PSA_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < psa_chunk_workspace_size(info) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PSA_ERR_WORKSPACE;
