@@ -595,6 +595,12 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+# Small calls cost what these checks cost: each property of a tensor is asked
+# for once (about 0.1 us), and in the order that needs the fewest.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_WEIGHT_DTYPES = {_BF16: PSA_BF16, _F32: PSA_F32}
+
+
 def _dense(t, shape, dtype, device, name: str):
     """A contiguous CUDA tensor of this shape, dtype and device."""
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
@@ -605,16 +611,14 @@ def _dense(t, shape, dtype, device, name: str):
 
 def _rows(t, dtype, device, name: str):
     """[T, H, d] with dense heads, tokens any distance apart: (T, H, d, token stride)."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 3 or t.dtype is not dtype or t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: a {dtype} CUDA tensor [T, H, d] is needed on {device}")
-    T, H, d = t.shape
+    T, H, d = shape
     st, sh, sd = t.stride()
-    if (H > 1 and sh != d) or sd != 1:
+    if (sh != d and H > 1) or sd != 1:
         raise ValueError(f"{name}: the heads of a token have to be dense")
     return T, H, d, st if T > 1 else H * d
-
-
-_WEIGHT_DTYPES = {torch.bfloat16: PSA_BF16, torch.float32: PSA_F32}
 
 
 def _norm_rope(T: int, d: int, device, positions, cos_sin, q_weight, k_weight, eps, interleaved):
@@ -624,28 +628,26 @@ def _norm_rope(T: int, d: int, device, positions, cos_sin, q_weight, k_weight, e
     if cos_sin is not None:
         if positions is None:
             raise ValueError("a rotation (cos_sin) needs positions")
-        if cos_sin.dim() != 2:
+        shape = cos_sin.shape
+        if len(shape) != 2:
             raise ValueError("cos_sin: [positions, rot_dim] is needed")
-        pos = _dense(positions, (T,), torch.int32, device, "positions").data_ptr()
-        n_pos, rot = cos_sin.shape
+        n_pos, rot = shape
         if n_pos == 0:
             raise ValueError("cos_sin: at least one position is needed")
-        cs = _dense(cos_sin, (n_pos, rot), torch.float32, device, "cos_sin").data_ptr()
-    if q_weight is not None:
-        wdt = _weight_dtype(q_weight, "q_weight")
-        qw = _dense(q_weight, (d,), q_weight.dtype, device, "q_weight").data_ptr()
-    if k_weight is not None:
-        if q_weight is not None and k_weight.dtype is not q_weight.dtype:
-            raise ValueError("q_weight and k_weight have to be of one dtype")
-        wdt = _weight_dtype(k_weight, "k_weight")
-        kw = _dense(k_weight, (d,), k_weight.dtype, device, "k_weight").data_ptr()
+        pos = _dense(positions, (T,), _I32, device, "positions").data_ptr()
+        cs = _dense(cos_sin, shape, _F32, device, "cos_sin").data_ptr()
+    if q_weight is not None or k_weight is not None:
+        dtype = (k_weight if q_weight is None else q_weight).dtype
+        wdt = _WEIGHT_DTYPES.get(dtype)
+        if wdt is None:
+            raise ValueError("q_weight, k_weight: bf16 or fp32 is needed")
+        if q_weight is not None:
+            qw = _dense(q_weight, (d,), dtype, device, "q_weight").data_ptr()
+        if k_weight is not None:
+            if k_weight.dtype is not dtype:
+                raise ValueError("q_weight and k_weight have to be of one dtype")
+            kw = _dense(k_weight, (d,), dtype, device, "k_weight").data_ptr()
     return ctypes.byref(NormRope(pos, cs, n_pos, rot, bool(interleaved), qw, kw, wdt, eps))
-
-
-def _weight_dtype(w, name: str) -> int:
-    if w.dtype not in _WEIGHT_DTYPES:
-        raise ValueError(f"{name}: bf16 or fp32 is needed")
-    return _WEIGHT_DTYPES[w.dtype]
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -660,18 +662,18 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     rotation).  Pairs are (i, i + rot_dim/2), or (2i, 2i + 1) with
     ``interleaved``; elements behind rot_dim pass through.  q_out and k_out may
     be q and k themselves (dense ones); other overlaps are refused."""
-    _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
-    dev = q.device
-    T, Hq, d, qs = _rows(q, q.dtype, dev, "q")
-    Tk, Hkv, dk, ks = _rows(k, q.dtype, dev, "k")
+    dtype, dev = q.dtype, q.device
+    code = _WEIGHT_DTYPES.get(dtype)
+    _need(code is not None, "q: bf16 or fp32 is needed")
+    T, Hq, d, qs = _rows(q, dtype, dev, "q")
+    Tk, Hkv, dk, ks = _rows(k, dtype, dev, "k")
     _need(Tk == T and dk == d, "q and k have to agree in tokens and head size")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     q_out = (torch.empty_like(q) if q_out is None
-             else _dense(q_out, (T, Hq, d), q.dtype, dev, "q_out"))
+             else _dense(q_out, (T, Hq, d), dtype, dev, "q_out"))
     k_out = (torch.empty_like(k) if k_out is None
-             else _dense(k_out, (T, Hkv, d), q.dtype, dev, "k_out"))
-    _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks,
-            _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how, q_out.data_ptr(),
+             else _dense(k_out, (T, Hkv, d), dtype, dev, "k_out"))
+    _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, code, T, Hq, Hkv, d, how, q_out.data_ptr(),
             k_out.data_ptr(), _addr(status))
     return q_out, k_out
 
@@ -684,31 +686,32 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_
     and None where there is no weight.  dq and dk may be given as slices of
     one gradient tensor (dense heads, any token stride of whole 16 bytes), or
     be the upstream gradients or the inputs themselves."""
-    _need(q.dtype in _WEIGHT_DTYPES, "q: bf16 or fp32 is needed")
-    dev = q.device
-    T, Hq, d, qs = _rows(q, q.dtype, dev, "q")
-    Tk, Hkv, hd, ks = _rows(k, q.dtype, dev, "k")
+    dtype, dev = q.dtype, q.device
+    code = _WEIGHT_DTYPES.get(dtype)
+    _need(code is not None, "q: bf16 or fp32 is needed")
+    T, Hq, d, qs = _rows(q, dtype, dev, "q")
+    Tk, Hkv, hd, ks = _rows(k, dtype, dev, "k")
     _need(Tk == T and hd == d, "q and k have to agree in tokens and head size")
-    _dense(dq_out, (T, Hq, d), q.dtype, dev, "dq_out")
-    _dense(dk_out, (T, Hkv, d), q.dtype, dev, "dk_out")
+    _dense(dq_out, (T, Hq, d), dtype, dev, "dq_out")
+    _dense(dk_out, (T, Hkv, d), dtype, dev, "dk_out")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     dqs, dks = Hq * d, Hkv * d
     if dq is None:
         dq = torch.empty_like(dq_out)
     else:
         _need(dq.shape == q.shape, "dq has to be shaped as q")
-        dqs = _rows(dq, q.dtype, dev, "dq")[3]
+        dqs = _rows(dq, dtype, dev, "dq")[3]
     if dk is None:
         dk = torch.empty_like(dk_out)
     else:
         _need(dk.shape == k.shape, "dk has to be shaped as k")
-        dks = _rows(dk, q.dtype, dev, "dk")[3]
-    dqw = None if q_weight is None else torch.empty_like(q_weight, dtype=torch.float32)
-    dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=torch.float32)
+        dks = _rows(dk, dtype, dev, "dk")[3]
+    dqw = None if q_weight is None else torch.empty_like(q_weight, dtype=_F32)
+    dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=_F32)
     if workspace is None:
         workspace = q.new_empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8)
     _launch("psa_qk_norm_rope_bwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, dq_out.data_ptr(),
-            dk_out.data_ptr(), _WEIGHT_DTYPES[q.dtype], T, Hq, Hkv, d, how,
+            dk_out.data_ptr(), code, T, Hq, Hkv, d, how,
             dq.data_ptr(), dqs, dk.data_ptr(), dks, _addr(dqw), _addr(dkw), workspace.data_ptr(),
             workspace.numel(), _addr(status))
     return dq, dk, dqw, dkw
@@ -726,7 +729,7 @@ def _caches(k_cache, v_cache, k_scale, v_scale, device):
         sc = ctypes.byref(KvScales(k_scale, v_scale))
         ok = k_cache.dtype in _E4M3_DTYPES and v_cache.dtype in _E4M3_DTYPES
     else:
-        ok = k_cache.dtype is torch.bfloat16 and v_cache.dtype is torch.bfloat16
+        ok = k_cache.dtype is _BF16 and v_cache.dtype is _BF16
     shape = k_cache.shape
     if (not ok or len(shape) != 3 or v_cache.shape != shape or not k_cache.is_contiguous()
             or not v_cache.is_contiguous() or not k_cache.is_cuda or k_cache.device != device
@@ -748,17 +751,17 @@ def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None,
     Two tokens may not share a row."""
     dev = k_cache.device
     ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
-    T, Hk, dk, ks = _rows(k, torch.bfloat16, dev, "k")
-    Tv, Hv, dv, vs = _rows(v, torch.bfloat16, dev, "v")
+    T, Hk, dk, ks = _rows(k, _BF16, dev, "k")
+    Tv, Hv, dv, vs = _rows(v, _BF16, dev, "v")
     _need((Hk, dk) == (Hkv, d) and (Tv, Hv, dv) == (T, Hkv, d),
           "k and v have to agree with the caches in heads and head size")
     Hq, qs = 0, 0
     if q is not None:
-        Tq, Hq, dq, qs = _rows(q, torch.bfloat16, dev, "q")
+        Tq, Hq, dq, qs = _rows(q, _BF16, dev, "q")
         _need(Tq == T and dq == d, "q, k and v have to agree in tokens and head size")
         q_out = (torch.empty_like(q) if q_out is None
-                 else _dense(q_out, (T, Hq, d), torch.bfloat16, dev, "q_out"))
-    _dense(slots, (T,), torch.int32, dev, "slots")
+                 else _dense(q_out, (T, Hq, d), _BF16, dev, "q_out"))
+    _dense(slots, (T,), _I32, dev, "slots")
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     _launch("psa_cache_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv,
             d, how, k_cache.data_ptr(), v_cache.data_ptr(), ntok, slots.data_ptr(),
@@ -773,11 +776,11 @@ def cache_read(k_cache, v_cache, rows, k_scale: float | None = None,
     dev = k_cache.device
     ntok, Hkv, d, sc = _caches(k_cache, v_cache, k_scale, v_scale, dev)
     n = rows.numel()
-    _dense(rows, (n,), torch.int32, dev, "rows")
-    k = (k_cache.new_empty((n, Hkv, d), dtype=torch.bfloat16) if k is None
-         else _dense(k, (n, Hkv, d), torch.bfloat16, dev, "k"))
+    _dense(rows, (n,), _I32, dev, "rows")
+    k = (k_cache.new_empty((n, Hkv, d), dtype=_BF16) if k is None
+         else _dense(k, (n, Hkv, d), _BF16, dev, "k"))
     v = (torch.empty_like(k) if v is None
-         else _dense(v, (n, Hkv, d), torch.bfloat16, dev, "v"))
+         else _dense(v, (n, Hkv, d), _BF16, dev, "v"))
     _launch("psa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), ntok, rows.data_ptr(),
             n, Hkv, d, sc, k.data_ptr(), v.data_ptr(), _addr(status))
     return k, v
