@@ -98,10 +98,10 @@ Plan plan_pieces(const std::vector<Block>& blocks, const std::vector<int32_t>& f
   return plan;
 }
 
-// Lists filled one after another up to `budget`, a block cut where a list is
+// Lists filled one after another up to the load `most`, a block cut where a list is
 // full: lists of equal cost with about one cut each.  Returns false if the
 // lists do not hold all.
-bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, double budget,
+bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, double most,
                 const std::vector<int32_t>& first, Plan& plan) {
   plan.pieces.clear();
   plan.longest = 0.0;
@@ -114,8 +114,8 @@ bool fill_lists(const std::vector<Block>& blocks, int32_t Hkv, int32_t n_ctas, d
         const int32_t n = k.tiles();
         for (int32_t t = 0; t < n;) {
           int32_t fit = n - t;
-          if (load + k.cost(fit) > budget) {
-            const double left = budget - load - kPieceCost - kSplitCost;
+          if (load + k.cost(fit) > most) {
+            const double left = most - load - kPieceCost - kSplitCost;
             fit = std::min(n - t, int32_t(left / k.tile_cost));
             // no stubs: a cut leaves at least two tiles on both sides
             if (n - t - fit < 2) fit = n - t - 2;
@@ -192,7 +192,7 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
       offer(plan_pieces(blocks, first, Hkv, n_ctas, len));
       if (len <= 0.5) break;
     }
-    // lists of one budget, the smallest that holds all (to 1 %)
+    // lists of at most one load, the smallest that holds all (to 1 %)
     Plan fill, tried;
     double low = total / n_ctas, high = 2.0 * low + 8.0;
     bool found = false;
