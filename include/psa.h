@@ -485,7 +485,7 @@ typedef struct psa_norm_rope {
     const void *q_weight;      /* device [d] */
     const void *k_weight;
     int32_t weight_dtype;      /* PSA_BF16 or PSA_F32 */
-    float eps;                 /* >= 0, finite */
+    float eps;                 /* >= 0, finite (0: a row of zeros becomes NaN) */
 } psa_norm_rope;
 
 /*

@@ -597,7 +597,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_bwd_kernel(RowParams p) {
           raw = Raw<T>{};
           if (row) raw.load(xr + i0 * D, pc.a, pc.b);
           raw.get(x);
-          const float r = rsqrtf(row_sum<LPR>(dot16(x, x)) * (1.f / D) + p.eps);
+          const float ms = row_sum<LPR>(dot16(x, x)) * (1.f / D);
+          // (without an eps a row of zeros has no root)
+          const float r = row ? rsqrtf(ms + p.eps) : 0.f;
           const uint64_t r2 = f2_pack(r, r);
           uint64_t wg[8];
 #pragma unroll

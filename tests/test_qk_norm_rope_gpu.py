@@ -435,3 +435,19 @@ def test_append_then_read_through_a_graph_on_another_stream():
     want_q, want_k = psa.qk_norm_rope(q, k, pos, cs, w, w, EPS)
     torch.cuda.synchronize()
     assert torch.equal(yq, want_q) and torch.equal(kk, want_k) and torch.equal(vv, v)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,dtype", [
+    (7, 5, 1, 128, torch.bfloat16),
+    (9, 2, 2, 128, torch.bfloat16),
+    (40, 9, 3, 64, torch.bfloat16),
+    (6, 3, 1, 256, torch.bfloat16),
+    (5, 3, 1, 256, torch.float32),
+    (11, 5, 2, 64, torch.float32),
+    (40001, 9, 1, 128, torch.bfloat16),
+])
+def test_backward_without_eps(T, Hq, Hkv, d, dtype, monkeypatch):
+    """eps = 0 is a norm like any other where no row is zero, also where a
+    token's heads do not fill a warp's last group of rows."""
+    monkeypatch.setitem(globals(), "EPS", 0.0)
+    test_backward(T, Hq, Hkv, d, d, False, dtype, torch.float32, True)
