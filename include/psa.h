@@ -627,8 +627,9 @@ size_t psa_chunk_workspace_size(const psa_chunk_info *info);
  * Token i of request b is at position kv_lens[b] - qo_lens[b] + i and sees the
  * keys up to its own position, the last `window` of them if the plan has a
  * window.  The cache must hold the new tokens' keys already
- * (psa_cache_append).  With an e4m3 cache |q| must stay below 65504 (queries
- * and probabilities are widened to f16 there).  A value (not a key) that is
+ * (psa_cache_append).  With an e4m3 cache queries and weights are f16: |q|
+ * must stay below 65504, elements of q below 2^-14 are off by up to 2^-25, and
+ * weights below 2^-21 of their row's largest by up to 2^-32 of it.  A value (not a key) that is
  * not finite spoils every row of its 256-row block that shares its tile, as
  * in psa_prefill_fwd; rows of other requests and unused cache rows are never
  * touched.

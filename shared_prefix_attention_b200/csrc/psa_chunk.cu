@@ -44,7 +44,9 @@
 // softmax, PV (about 3400 cycles) is longer than either's share of it (2050),
 // and two halves are all that TMEM holds.
 // P is rounded to bf16 (f16 over an e4m3 cache) for the tensor cores: at most
-// half a step per weight, averaged over the keys; the sum l keeps fp32.
+// half a step per weight, averaged over the keys; the sum l keeps fp32.  f16
+// steps stop shrinking at 2^-14, so those weights are held 2^7 up (kLift): one
+// far below the row's largest is off by at most 2^-32 of it.
 // Every wait is bounded.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -78,6 +80,11 @@ constexpr int threads() { return WIDE ? 512 : 384; }
 static_assert(128 * kRegsLow + 256 * kRegsSoftmax <= threads<false>() * kRegsLaunch,
               "register split");
 constexpr float kRescaleLog2 = 8.f;
+// Weights are 2^(logit - max + kLift): with a max that lags by kRescaleLog2 at
+// most 2^15, which f16 holds (65504).  Unlifted, 64k equal keys beside one with
+// 99 % of the weight had weights of 2 to 4 steps each: o was 5.5 % off.
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
 constexpr uint32_t kTmemCols = 512;  // per half: S at X*256, O at X*256 + 128
 
 template <int D, bool E4M3, bool WIDE>
@@ -272,7 +279,7 @@ __device__ __forceinline__ float to_log2(float s, const Params& p) {
     return s * p.scale_log2;
 }
 
-// Weights of a row of logits against the max -neg_m, packed in pairs into the
+// Weights of a row of logits, 2^(logit + neg_m), packed in pairs into the
 // row's first half (pair k over logit k <= 2 k, which is done by then);
 // returns their fp32 sum.
 template <bool F16, int N, int K0 = 0, int K1 = N / 2>
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(threads<WIDE>(), 1)
             l_run *= alpha;
             m_run = m_tile;
           }
-          return m_run == -INFINITY ? 0.f : -m_run;
+          return m_run == -INFINITY ? 0.f : kLift<E4M3> - m_run;
         };
         if constexpr (CAP || WIDE) {
           // half a row at a time, read twice: a capped weight needs more
@@ -882,7 +889,7 @@ __global__ void __launch_bounds__(threads<WIDE>(), 1)
       if (!mbar_wait(pv_done + x, (sc_count - 1) & 1, &abort_flag, p.status)) break;
       tc_fence_after();
       const float inv = l_run == 0.f ? 0.f : p.v_scale / l_run;
-      const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
+      const float lse2 = l_run == 0.f ? -INFINITY : m_run - kLift<E4M3> + __log2f(l_run);
       const size_t row = size_t(w.q0 + (w.twin ? 0 : x * p.TPH) + tok) * p.Hq + w.kvh * p.G + g;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
