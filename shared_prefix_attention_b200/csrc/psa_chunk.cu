@@ -227,8 +227,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// Logits outside [lo, hi) become -inf (their weights exactly 0).
-template <int N>
+// Logits outside [lo, hi) become the mark of a masked one, whose weight is
+// exactly 0: -inf, or with a cap the lowest finite number, since a logit of
+// -inf (an infinite key) has the weight of -c there.  (Finding the masked ones
+// by their positions again took 2 % longer than comparing with the mark.)
+template <bool CAP>
+constexpr uint32_t kMasked = CAP ? 0xff7fffffu : 0xff800000u;
+template <bool CAP, int N>
 __device__ __forceinline__ void mask_row(uint32_t (&s)[N], int lo, int hi) {
 #pragma unroll
   for (int w = 0; w < N / 32; ++w) {
@@ -238,7 +243,7 @@ __device__ __forceinline__ void mask_row(uint32_t (&s)[N], int lo, int hi) {
     const uint32_t keep = below_b & ~below_a;
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (!((keep >> k) & 1u)) s[32 * w + k] = __float_as_uint(-INFINITY);
+      if (!((keep >> k) & 1u)) s[32 * w + k] = kMasked<CAP>;
   }
 }
 
@@ -346,8 +351,8 @@ __device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_
       f2_unpack(y[j], x0, x1);
       float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
       if (MASKED) {
-        p0 = s[4 * k + 2 * j] == 0xff800000u ? 0.f : p0;
-        p1 = s[4 * k + 2 * j + 1] == 0xff800000u ? 0.f : p1;
+        p0 = s[4 * k + 2 * j] == kMasked<true> ? 0.f : p0;
+        p1 = s[4 * k + 2 * j + 1] == kMasked<true> ? 0.f : p1;
       }
       acc[j] = f2_add(acc[j], f2_pack(p0, p1));
       // packed behind the four's last use of its logits
@@ -822,15 +827,20 @@ __global__ void __launch_bounds__(threads<WIDE>(), 1)
           for (int c = 0; c < 2; ++c) {
             tmem_ld64(tS + c * (BN / 2), sr);
             tmem_wait_ld();
-            if (masked) mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+            if (masked) mask_row<CAP>(sr, lo - c * (BN / 2), hi - c * (BN / 2));
             mx = fmaxf(mx, max_of_row(sr));
+          }
+          if constexpr (CAP) {
+            // no logit above the lowest: none is seen, or those seen are at -c
+            const float lowest = __uint_as_float(kMasked<true>);
+            if (mx <= lowest) mx = lo < min(hi, BN) ? lowest : -INFINITY;
           }
           const float neg_m = raise(to_log2<CAP>(mx, p));
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             tmem_ld64(tS + c * (BN / 2), sr);
             tmem_wait_ld();
-            if (masked) mask_row(sr, lo - c * (BN / 2), hi - c * (BN / 2));
+            if (masked) mask_row<CAP>(sr, lo - c * (BN / 2), hi - c * (BN / 2));
             if constexpr (!CAP)
               l_run += weights_row<E4M3>(sr, neg_m, p);
             else if (masked)
@@ -844,7 +854,7 @@ __global__ void __launch_bounds__(threads<WIDE>(), 1)
           uint32_t sr[BN];
           tmem_ld128(tS, sr);
           tmem_wait_ld();
-          if (masked) mask_row(sr, lo, hi);
+          if (masked) mask_row<CAP>(sr, lo, hi);
           const float neg_m = raise(to_log2<CAP>(max_of_row(sr), p));
           l_run += weights_row<E4M3, BN, 0, BN / 4>(sr, neg_m, p);
           tmem_st32(tS, *reinterpret_cast<uint32_t(*)[BN / 4]>(sr));

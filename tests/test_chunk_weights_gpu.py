@@ -1,5 +1,5 @@
 """Chunk attention where the softmax weights are hard to hold: one key far above
-many small ones."""
+many small ones, infinite logits under a cap."""
 import ctypes
 import math
 
@@ -78,3 +78,51 @@ def test_one_dominant_key_of_value_zero(n, L, Hq, Hkv, d, paged, cap, share, kin
     over = float(((o.double() - ro).abs() / tol).max())
     assert over <= 1, f"{over:.2f} times the bound, o off by " \
         f"{float((o.double() - ro).norm() / ro.norm()):.2%}"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,L", [(1, 1), (3, 300), (300, 500)])
+def test_infinite_logits_reach_the_cap(n, L, kind):
+    """c tanh(+-inf / c) is +-c: keys of one infinite element (bf16 caches), and
+    products beyond fp32, weigh as keys at the cap, in whole and in partial
+    tiles; a row that sees nothing else has their mean.  Weights and values are
+    few and small, so the bound is the rounding of weights and store."""
+    Hq, Hkv, d, cap = 4, 2, 128, 5.0
+    g = torch.Generator().manual_seed(n + L)
+    q = torch.zeros(n, Hq, d)
+    q[..., 0] = torch.where(torch.rand(n, Hq, generator=g) < 0.5, -1.0, 1.0)
+    q[..., 1] = 1.0
+    k = torch.zeros(L, Hkv, d)
+    k[..., 1] = torch.randint(-2, 3, (L, Hkv), generator=g).float()
+    far = torch.rand(L, Hkv, generator=g) < 0.3
+    far[:max(1, L // 4)] = True  # the first rows see these alone
+    v = torch.randint(-4, 5, (L, Hkv, d), generator=g).float()
+    ks = vs = None
+    if kind == "bf16":
+        k[..., 0] = torch.where(far, -math.inf, 0.0)
+        q, k, v, scale = q.bfloat16().cuda(), k.bfloat16().cuda(), v.bfloat16().cuda(), 1.0
+        logits = k.double()
+    else:
+        ks = vs = 1.0
+        k[..., 0] = torch.where(far, -256.0, 0.0)
+        scale = 2.0 ** 100  # with the scale 256 is beyond any cap; 2 * 2^100 as well
+        q, k, v = q.bfloat16().cuda(), k.to(F8).cuda(), v.to(F8).cuda()
+        logits = k.float().double()
+    o, lse = psa.chunk(q, k, v, psa.plan_chunk([n], [L], Hq, Hkv, d), scale, logit_cap=cap,
+                       k_scale=ks, v_scale=vs)
+    G = Hq // Hkv
+    qq = q.double().unflatten(1, (Hkv, G))
+    s = (qq[..., 0, None] * logits[..., 0].T[None, :, None]).nan_to_num(0.0, posinf=1e30, neginf=-1e30)
+    s = (s + qq[..., 1, None] * logits[..., 1].T[None, :, None]) * scale  # [n, Hkv, G, L]
+    s = cap * torch.tanh(s / cap)
+    s = s.masked_fill(~see_of(n, L)[:, None, None], -math.inf)
+    rl = torch.logsumexp(s, -1)
+    p = torch.exp(s - rl[..., None])
+    vv = v.float().double()
+    ro = torch.einsum("nhgl,lhd->nhgd", p, vv).flatten(1, 2)
+    A = torch.einsum("nhgl,lhd->nhgd", p, vv.abs()).flatten(1, 2)
+    e = 24 * U * cap + 2.0 ** -20
+    assert torch.isfinite(lse).all() and torch.isfinite(o.float()).all()
+    assert float((lse.double() - rl.flatten(1)).abs().max()) <= e
+    tol = (2.0 ** -8 + 2 * e) * A + 2.0 ** -8 * ro.abs() + 1e-30
+    assert float(((o.double() - ro).abs() - tol).max()) <= 0
