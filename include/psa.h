@@ -620,7 +620,7 @@ size_t psa_chunk_workspace_size(const psa_chunk_info *info);
  *              PSA_ERR_INVALID_ARG in dev_status
  *   logit_cap  0: none; c > 0: logits become c tanh(logit / c) before the mask
  *              (c <= 1000, PSA_ERR_UNSUPPORTED above: the cap is formed with an
- *              error of about 2^-22 c)
+ *              error of at most 1.5 * 2^-20 c)
  *   o          device [T, Hq, d] bf16 (written up to n_rows; PSA_ERR_INVALID_ARG if
  *              it overlaps q or a cache)
  *   lse        device [T, Hq] fp32 (written up to n_rows; nullable)

@@ -273,7 +273,7 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t M, uint32_t N, bool b_m
 }
 
 // The log2-domain logit of a raw one.  Capped: c tanh(s / c) = c - 2 c / (1 +
-// exp(2 s / c)); its error is absolute (a few 1e-7 c), as the weights need it.
+// exp(2 s / c)); its error is absolute (1.4e-6 c at most), as a weight needs it.
 template <bool CAP>
 __device__ __forceinline__ float to_log2(float s, const Params& p) {
   if constexpr (CAP)
@@ -317,7 +317,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // c' / (1 + e)), c' = c log2(e): two exponentials and a reciprocal, which would
 // leave the special-function unit a third of the uncapped rate.  So four
 // reciprocals come from that of the four's product (e is held below 2^30,
-// where the cap is reached to 1e-9, so the product stays finite).  A further
+// where the cap is reached to 1e-9, so the product stays finite).  With U half a
+// step of fp32, 1 / (1 + e) is off by 7 U of itself (sum, two products, 2 U of
+// the reciprocal, two products) and 2 U (a quarter of the exponential's and its
+// argument's), which counts twice c'; c', the offset, the last sum: 24 U c' in
+// all (test: logits to 4.5 c at c = 1000).  A further
 // step, a part of the first exponentials by a polynomial on the FMA pipe,
 // gained 2 %: the issue slots are then as full as the unit.
 template <bool F16, bool MASKED, int N>

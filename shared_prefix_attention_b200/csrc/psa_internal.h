@@ -191,7 +191,8 @@ int launch_cache_read(const CacheReadArgs& a);
 // ---------------------------------------------------------------- chunk
 
 // The largest logit cap: c tanh(s / c) is formed as c - 2 c / (1 + exp(2 s /
-// c)), off by about 2^-22 c, here at most 2.4e-4.
+// c)), off by at most 24 half steps of fp32, 1.5 2^-20 c (weights_row_capped),
+// here 1.4e-3: less than the rounding of a weight to bf16 (2^-8).
 constexpr float kChunkMaxCap = 1000.f;
 
 struct ChunkArgs {

@@ -1,5 +1,5 @@
 """Chunk attention where the softmax weights are hard to hold: one key far above
-many small ones, infinite logits under a cap."""
+many small ones, logits that are infinite or at the largest cap."""
 import ctypes
 import math
 
@@ -125,4 +125,41 @@ def test_infinite_logits_reach_the_cap(n, L, kind):
     assert torch.isfinite(lse).all() and torch.isfinite(o.float()).all()
     assert float((lse.double() - rl.flatten(1)).abs().max()) <= e
     tol = (2.0 ** -8 + 2 * e) * A + 2.0 ** -8 * ro.abs() + 1e-30
+    assert float(((o.double() - ro).abs() - tol).max()) <= 0
+
+
+@pytest.mark.parametrize("cap", [1000.0, 50.0])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_error_of_the_capped_logit(cap, kind):
+    """Logits that are exact in fp32 (one product each), strongly negative and
+    positive ones mixed, at the largest cap: what is left is the error of c
+    tanh(s / c).  Four reciprocals come from one: with U half a step, 1 / (1 + e)
+    carries 7 U (the sum, three products, two for the reciprocal, two more
+    products less one that cancels), the exponential's 4 U and the 4 U of its
+    argument's factors count a quarter of it; all that twice the cap, and the
+    products with c, the offset and the last sum add 6 U of the cap: 24 U c.  The
+    log-sum-exp is rounded as a partial's, as the row's and in the change of base."""
+    Hq, Hkv, d, n, L = 4, 2, 64, 40, 1000
+    g = torch.Generator().manual_seed(int(cap))
+    q = torch.zeros(n, Hq, d, dtype=torch.bfloat16)
+    q[..., 0] = torch.randint(64, 96, (n, Hq), generator=g).bfloat16()
+    pick = torch.tensor([-12.0, -3.0, -0.125, 0.0, 0.25, 10.0, 11.0, 12.0])
+    k = torch.zeros(L, Hkv, d)
+    k[..., 0] = pick[torch.randint(0, 8, (L, Hkv), generator=g)]
+    v = torch.randint(-8, 9, (L, Hkv, d), generator=g).float()
+    scale = cap / 256.0  # 96 * 12 / 256: up to 4.5 caps
+    ks = vs = None
+    if kind == "e4m3":
+        ks = vs = 1.0
+        k, v = k.to(F8).cuda(), v.to(F8).cuda()
+    else:
+        k, v = k.bfloat16().cuda(), v.bfloat16().cuda()
+    q = q.cuda()
+    o, lse = psa.chunk(q, k, v, psa.plan_chunk([n], [L], Hq, Hkv, d), scale, logit_cap=cap,
+                       k_scale=ks, v_scale=vs)
+    ro, rl, A, _ = reference(q, values(k, ks), values(v, vs), [n], [L], None, scale, 0, cap)
+    e = 24 * U * cap + 4 * U * rl.abs()
+    assert float(((lse.double() - rl).abs() - e).max()) <= 0
+    h = 2.0 ** -11 if ks else 2.0 ** -8
+    tol = (h + 2 * e[..., None]) * A + 2.0 ** -8 * ro.abs()
     assert float(((o.double() - ro).abs() - tol).max()) <= 0
