@@ -798,17 +798,34 @@ class ChunkPlan:
         self._shape = (info.Hq, info.Hkv, info.head_dim, info.n_keys)
 
 
+_INT32_MAX = 2**31 - 1
+
+
+def _int32s(x, name: str):
+    """x as int32 values, none of them changed on the way."""
+    given = np.asarray(x)
+    with np.errstate(invalid="ignore"):
+        out = given.astype(np.int32)
+    if not (out == given).all():
+        raise ValueError(f"{name}: whole numbers of 32 bits are needed")
+    return out
+
+
 def build_chunk_plan(qo_lens, kv_lens, Hq: int, Hkv: int, head_dim: int, window: int = 0,
                      n_ctas: int = 148):
     """(plan as a host int32 array, ChunkInfo) for ``n_ctas`` work lists."""
-    ql = np.ascontiguousarray(np.asarray(qo_lens, dtype=np.int32))
-    kl = np.ascontiguousarray(np.asarray(kv_lens, dtype=np.int32))
+    ql = np.ascontiguousarray(_int32s(qo_lens, "qo_lens"))
+    kl = np.ascontiguousarray(_int32s(kv_lens, "kv_lens"))
     _need(ql.ndim == 1 and ql.shape == kl.shape, "one query and one key length per request")
+    # a window beyond every key is no window
+    Hq, Hkv, head_dim, window, n_ctas = _int32s(
+        [Hq, Hkv, head_dim, min(window, _INT32_MAX), n_ctas],
+        "Hq, Hkv, head_dim, window, n_ctas").tolist()
     info = ChunkInfo()
     out = np.zeros(4096, dtype=np.int32)
     while True:
         rc = lib().psa_build_chunk_plan(_ptr(ql), _ptr(kl), len(ql), Hq, Hkv, head_dim,
-                                        int(window), n_ctas, _ptr(out), len(out),
+                                        window, n_ctas, _ptr(out), len(out),
                                         ctypes.byref(info))
         if rc == PSA_ERR_CAPACITY and info.len > len(out):
             out = np.zeros(info.len, dtype=np.int32)

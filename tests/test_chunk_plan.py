@@ -294,3 +294,42 @@ def test_large_batches_are_planned_quickly():
     t = time.perf_counter()
     _, info = psa.build_chunk_plan([1] * 4096, [1000 + i % 700 for i in range(4096)], 32, 8, 128)
     assert info.n_units >= 4096 * 8 and time.perf_counter() - t < 0.5
+
+
+WIDE = 2**32
+
+
+@pytest.mark.parametrize("args", [
+    ([1], np.array([WIDE + 100]), 8, 2, 128),
+    (np.array([WIDE + 1]), [100], 8, 2, 128),
+    (torch.tensor([1]), torch.tensor([WIDE + 100]), 8, 2, 128),
+    (np.array([1], dtype=np.uint64), np.array([2**64 - 1], dtype=np.uint64), 8, 2, 128),
+    ([1], [WIDE + 100], 8, 2, 128),
+    ([1], [100.5], 8, 2, 128),
+    ([0.5], [100], 8, 2, 128),
+    ([1], [float("nan")], 8, 2, 128),
+    ([[1]], [[100]], 8, 2, 128),
+    ([1], [100], WIDE + 8, 2, 128),
+    ([1], [100], 8, WIDE + 2, 128),
+    ([1], [100], 8, 2, WIDE + 128),
+    ([1], [100], 8, 2, 128, 0, WIDE + 148),
+    ([1], [100], 8, 2, 128, 4.5),
+    ([1], [100], 8, 2, 128, -WIDE),
+])
+def test_plan_arguments_beyond_32_bits_are_refused(args):
+    """No length, head count or window becomes another one on its way to the
+    planner's 32-bit integers."""
+    with pytest.raises((ValueError, psa.PsaError)):
+        psa.build_chunk_plan(*args)
+
+
+def test_plan_takes_any_integers_and_windows_beyond_every_key():
+    want, _ = psa.build_chunk_plan([3, 1], [700, 9], 8, 2, 128)
+    for ql, kl in ((np.array([3, 1]), np.array([700, 9], dtype=np.uint16)),
+                   (torch.tensor([3, 1]), torch.tensor([700, 9], dtype=torch.int32)),
+                   ((3, 1), (700.0, 9.0))):
+        assert (psa.build_chunk_plan(ql, kl, 8, 2, 128)[0] == want).all()
+    whole = decode(*psa.build_chunk_plan([3, 1], [700, 9], 8, 2, 128, 2**31 - 1))[1]
+    for window in (700, WIDE + 5, 2**70):
+        data, info = psa.build_chunk_plan([3, 1], [700, 9], 8, 2, 128, window)
+        assert (decode(data, info)[1] == whole).all() and info.window >= 700
