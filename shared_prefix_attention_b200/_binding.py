@@ -590,6 +590,22 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _word(status, device):
+    """Address of the status word."""
+    if status is None:
+        return None
+    if status.dtype is not _I32 or status.device != device or status.numel() < 1:
+        raise ValueError(f"status: an int32 tensor on {device} is needed")
+    return status.data_ptr()
+
+
+def _scratch(workspace, device):
+    """A caller's workspace: dense bytes."""
+    if workspace.dtype is not torch.uint8 or workspace.device != device \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous uint8 tensor on {device} is needed")
+
+
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
@@ -674,7 +690,7 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     k_out = (torch.empty_like(k) if k_out is None
              else _dense(k_out, (T, Hkv, d), dtype, dev, "k_out"))
     _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, code, T, Hq, Hkv, d, how, q_out.data_ptr(),
-            k_out.data_ptr(), _addr(status))
+            k_out.data_ptr(), _word(status, dev))
     return q_out, k_out
 
 
@@ -710,10 +726,12 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, cos_sin, q_weight=None, k_
     dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=_F32)
     if workspace is None:
         workspace = q.new_empty(lib().psa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8)
+    else:
+        _scratch(workspace, dev)
     _launch("psa_qk_norm_rope_bwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, dq_out.data_ptr(),
             dk_out.data_ptr(), code, T, Hq, Hkv, d, how,
             dq.data_ptr(), dqs, dk.data_ptr(), dks, _addr(dqw), _addr(dkw), workspace.data_ptr(),
-            workspace.numel(), _addr(status))
+            workspace.numel(), _word(status, dev))
     return dq, dk, dqw, dkw
 
 
@@ -765,7 +783,7 @@ def cache_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None,
     how = _norm_rope(T, d, dev, positions, cos_sin, q_weight, k_weight, eps, interleaved)
     _launch("psa_cache_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv,
             d, how, k_cache.data_ptr(), v_cache.data_ptr(), ntok, slots.data_ptr(),
-            sc, _addr(q_out) if q is not None else None, _addr(status))
+            sc, _addr(q_out) if q is not None else None, _word(status, dev))
     return q_out if q is not None else None
 
 
@@ -782,7 +800,7 @@ def cache_read(k_cache, v_cache, rows, k_scale: float | None = None,
     v = (torch.empty_like(k) if v is None
          else _dense(v, (n, Hkv, d), _BF16, dev, "v"))
     _launch("psa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), ntok, rows.data_ptr(),
-            n, Hkv, d, sc, k.data_ptr(), v.data_ptr(), _addr(status))
+            n, Hkv, d, sc, k.data_ptr(), v.data_ptr(), _word(status, dev))
     return k, v
 
 
@@ -879,7 +897,9 @@ def chunk(q, k_cache, v_cache, plan: ChunkPlan, scale: float, kv_indices=None,
            else _dense(lse, (T, Hq), torch.float32, dev, "lse"))
     if workspace is None:
         workspace = q.new_empty(plan.workspace_bytes, dtype=torch.uint8)
+    else:
+        _scratch(workspace, dev)
     _launch("psa_chunk_fwd", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ntok,
             _addr(kv_indices), sc, out.data_ptr(), lse.data_ptr(), T, scale, logit_cap, plan._ref,
-            plan.data.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status))
+            plan.data.data_ptr(), workspace.data_ptr(), workspace.numel(), _word(status, dev))
     return out, lse
