@@ -290,7 +290,7 @@ def plan_prefill(segments, cu_seqlens, head_dim: int, device="cuda") -> torch.Te
 def prefill(q, k, v, schedule: torch.Tensor, scale: float, out=None, lse=None,
             workspace=None, status=None):
     """O [T, Hq, d] (q's dtype) and LSE [T, Hq] fp32 over the flat layout."""
-    _require_cuda(q, k, v, schedule)
+    _require_cuda(q, k, v, schedule, out, lse, workspace)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     dtype = {torch.bfloat16: PSA_BF16, torch.float32: PSA_F32}[q.dtype]
@@ -301,7 +301,7 @@ def prefill(q, k, v, schedule: torch.Tensor, scale: float, out=None, lse=None,
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     rc = lib().psa_prefill_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), dtype, T, Hq,
                                Hkv, d, float(scale), _ptr(schedule), schedule.numel(),
-                               _ptr(workspace), workspace.numel(), _ptr(status),
+                               _ptr(workspace), workspace.numel(), _word(status, q.device),
                                _stream(q.device))
     _check(rc, "psa_prefill_fwd")
     return out, lse
@@ -320,7 +320,8 @@ def verify(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch.Tensor,
            workspace=None, status=None, features: VerifyFeatures | None = None,
            kv_indices=None):
     """Split-KV verify.  kv_indptr: device int32 [B+1] prefix offsets."""
-    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr)
+    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr, out, lse, workspace,
+                  kv_indices)
     BL, Hq, d = q_draft.shape
     Hkv = k_cache.shape[1]
     B = BL // Ld
@@ -336,7 +337,7 @@ def verify(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch.Tensor,
                               int(max_prefix_len), _ptr(kv_indices), _ptr(out), _ptr(lse), B,
                               Ld, Hq, Hkv, d, float(scale), nsplit,
                               ctypes.byref(features) if features is not None else None,
-                              _ptr(workspace), workspace.numel(), _ptr(status),
+                              _ptr(workspace), workspace.numel(), _word(status, q_draft.device),
                               _stream(q_draft.device))
     _check(rc, "psa_verify_fwd")
     return out, lse
@@ -349,7 +350,7 @@ def verify_noalloc(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch
     device scratch replaces the workspace (for callers that cannot allocate
     device memory at the call site).  Outputs are allocated here only for
     convenience; pass ``out`` / ``lse`` to avoid that too."""
-    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr)
+    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr, out, lse)
     BL, Hq, d = q_draft.shape
     Hkv = k_cache.shape[1]
     if Ld <= 0 or BL % Ld != 0:
@@ -362,20 +363,20 @@ def verify_noalloc(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch
                                       _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
                                       _ptr(kv_indptr), int(max_prefix_len), None, _ptr(out),
                                       _ptr(lse), B, Ld, Hq, Hkv, d, float(scale), nsplit, None,
-                                      _ptr(status), _stream(q_draft.device))
+                                      _word(status, q_draft.device), _stream(q_draft.device))
     _check(rc, "psa_verify_fwd_noalloc")
     return out, lse
 
 
 def sparse_latent(q, latent, idx, scale: float, out=None, lse=None, status=None):
     """Shared-latent sparse attention: O [T, H, dl] bf16, LSE [T, H] fp32."""
-    _require_cuda(q, latent, idx)
+    _require_cuda(q, latent, idx, out, lse)
     T, H, dl = q.shape
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
     rc = lib().psa_sparse_latent_fwd(_ptr(q), _ptr(latent), _ptr(idx), _ptr(out), _ptr(lse), T,
                                      latent.shape[0], H, dl, idx.shape[1], float(scale),
-                                     _ptr(status), _stream(q.device))
+                                     _word(status, q.device), _stream(q.device))
     _check(rc, "psa_sparse_latent_fwd")
     return out, lse
 
@@ -405,7 +406,8 @@ def verify_shared(q_draft, k_draft, v_draft, k_prefix, v_prefix, scale: float, L
     """Verify against one prefix shared by every request: O [B*Ld, Hq, d]
     bf16 and LSE [B*Ld, Hq] fp32; k_prefix/v_prefix [L, Hkv, d].  With
     draft_mask (device uint8 [B*Ld, Ld]) the draft block is that tree mask."""
-    _require_cuda(q_draft, k_draft, v_draft, k_prefix, v_prefix)
+    _require_cuda(q_draft, k_draft, v_draft, k_prefix, v_prefix, out, lse, workspace,
+                  draft_mask)
     BL, Hq, d = q_draft.shape
     Hkv = k_draft.shape[1]
     B = BL // Ld
@@ -420,14 +422,14 @@ def verify_shared(q_draft, k_draft, v_draft, k_prefix, v_prefix, scale: float, L
     if draft_mask is None:
         rc = lib().psa_verify_shared_fwd(_ptr(q_draft), _ptr(k_draft), _ptr(v_draft), kp, vp, L,
                                          _ptr(out), _ptr(lse), B, Ld, Hq, Hkv, d, float(scale), ns,
-                                         _ptr(workspace), workspace.numel(), _ptr(status),
-                                         _stream(q_draft.device))
+                                         _ptr(workspace), workspace.numel(),
+                                         _word(status, q_draft.device), _stream(q_draft.device))
         _check(rc, "psa_verify_shared_fwd")
     else:
         rc = lib().psa_verify_shared_tree_fwd(_ptr(q_draft), _ptr(k_draft), _ptr(v_draft), kp, vp,
                                               L, _ptr(draft_mask), _ptr(out), _ptr(lse), B, Ld,
                                               Hq, Hkv, d, float(scale), ns, _ptr(workspace),
-                                              workspace.numel(), _ptr(status),
+                                              workspace.numel(), _word(status, q_draft.device),
                                               _stream(q_draft.device))
         _check(rc, "psa_verify_shared_tree_fwd")
     return out, lse
@@ -440,7 +442,8 @@ def verify_fp8(q_draft, k_draft, v_draft, k_cache8, v_cache8, k_scale: float, v_
     """Split-KV verify over an e4m3 prefix cache (uint8 or float8_e4m3fn
     tensors [Ntok, Hkv, d]) standing for k_scale * e4m3 and v_scale * e4m3;
     kv_indices: optional token-granular page table (device int32)."""
-    _require_cuda(q_draft, k_draft, v_draft, k_cache8, v_cache8, kv_indptr)
+    _require_cuda(q_draft, k_draft, v_draft, k_cache8, v_cache8, kv_indptr, out, lse,
+                  workspace, kv_indices)
     BL, Hq, d = q_draft.shape
     Hkv = k_draft.shape[1]
     B = BL // Ld
@@ -455,7 +458,7 @@ def verify_fp8(q_draft, k_draft, v_draft, k_cache8, v_cache8, k_scale: float, v_
                                   int(max_prefix_len), _ptr(kv_indices), float(k_scale),
                                   float(v_scale),
                                   _ptr(out), _ptr(lse), B, Ld, Hq, Hkv, d, float(scale), ns, None,
-                                  _ptr(workspace), workspace.numel(), _ptr(status),
+                                  _ptr(workspace), workspace.numel(), _word(status, q_draft.device),
                                   _stream(q_draft.device))
     _check(rc, "psa_verify_fp8_fwd")
     return out, lse
@@ -483,7 +486,7 @@ def prefill_bwd(q, k, v, o, lse, dout, schedules, scale: float, dq=None, dk=None
     """Gradients (dq, dk, dv) of the prefill output for upstream gradient
     ``dout``; ``schedules`` from :func:`plan_prefill_bwd`."""
     sq, skv = schedules
-    _require_cuda(q, k, v, o, lse, dout, sq, skv)
+    _require_cuda(q, k, v, o, lse, dout, sq, skv, dq, dk, dv, workspace)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     dq = torch.empty_like(q) if dq is None else dq
@@ -495,7 +498,7 @@ def prefill_bwd(q, k, v, o, lse, dout, schedules, scale: float, dq=None, dk=None
     rc = lib().psa_prefill_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout),
                                _ptr(dq), _ptr(dk), _ptr(dv), T, Hq, Hkv, d, float(scale),
                                _ptr(sq), sq.numel(), _ptr(skv), skv.numel(), _ptr(workspace),
-                               workspace.numel(), _ptr(status), _stream(q.device))
+                               workspace.numel(), _word(status, q.device), _stream(q.device))
     _check(rc, "psa_prefill_bwd")
     return dq, dk, dv
 
@@ -505,7 +508,8 @@ def verify_tree(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch.Te
                 nsplit: int = 0, out=None, lse=None, workspace=None, status=None,
                 kv_indices=None):
     """Split-KV verify with a custom draft mask (device uint8 [B*Ld, Ld])."""
-    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr, draft_mask)
+    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr, draft_mask, out,
+                  lse, workspace, kv_indices)
     BL, Hq, d = q_draft.shape
     Hkv = k_draft.shape[1]
     B = BL // Ld
@@ -522,7 +526,7 @@ def verify_tree(q_draft, k_draft, v_draft, k_cache, v_cache, kv_indptr: torch.Te
                                    _ptr(out),
                                    _ptr(lse), B, Ld, Hq, Hkv, d, float(scale), ns,
                                    ctypes.byref(feat), _ptr(workspace), workspace.numel(),
-                                   _ptr(status), _stream(q_draft.device))
+                                   _word(status, q_draft.device), _stream(q_draft.device))
     _check(rc, "psa_verify_tree_fwd")
     return out, lse
 
@@ -537,7 +541,8 @@ def verify_extend(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr: torch.
     kv_indices[t]) and optional per-request tree masks (flat device uint8,
     request b's Lb x Lb block at mask_indptr[b]).  With k_scale / v_scale the
     caches hold e4m3 bytes standing for k_scale * e4m3 and v_scale * e4m3."""
-    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr, kv_indptr)
+    _require_cuda(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr, kv_indptr, out,
+                  lse, workspace, kv_indices, draft_mask, mask_indptr)
     NR, Hq, d = q_draft.shape
     Hkv = k_draft.shape[1]
     B = qo_indptr.numel() - 1
@@ -557,7 +562,8 @@ def verify_extend(q_draft, k_draft, v_draft, k_cache, v_cache, qo_indptr: torch.
                                      int(max_prefix_len), _ptr(kv_indices), _ptr(draft_mask),
                                      _ptr(mask_indptr), sc, _ptr(out), _ptr(lse), B, Hq, Hkv, d,
                                      float(scale), ns, ctypes.byref(feat), _ptr(workspace),
-                                     workspace.numel(), _ptr(status), _stream(q_draft.device))
+                                     workspace.numel(), _word(status, q_draft.device),
+                                     _stream(q_draft.device))
     _check(rc, "psa_verify_extend_fwd")
     return out, lse
 
@@ -689,8 +695,8 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
              else _dense(q_out, (T, Hq, d), dtype, dev, "q_out"))
     k_out = (torch.empty_like(k) if k_out is None
              else _dense(k_out, (T, Hkv, d), dtype, dev, "k_out"))
-    _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, code, T, Hq, Hkv, d, how, q_out.data_ptr(),
-            k_out.data_ptr(), _word(status, dev))
+    _launch("psa_qk_norm_rope_fwd", dev, q.data_ptr(), qs, k.data_ptr(), ks, code, T, Hq, Hkv, d,
+            how, q_out.data_ptr(), k_out.data_ptr(), _word(status, dev))
     return q_out, k_out
 
 

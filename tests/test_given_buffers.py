@@ -101,3 +101,73 @@ def test_layer_calls_check_the_workspace(call, launched):
     assert not launched
     call()
     assert len(launched) == 1
+
+
+# ---------------------------------------------------------------- the other attention calls
+
+class Lib:
+    """Stands for the loaded library: sizes are 256, calls are recorded."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def fn(*args):
+            if name.endswith("_size") or name.endswith("_splits"):
+                return 256
+            self.calls.append(name)
+            return psa.PSA_OK
+        return fn
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Lib()
+    monkeypatch.setattr(B, "_lib", lib)
+    monkeypatch.setattr(B, "_stream", lambda device: None)
+    return lib
+
+
+Q, KV, ROW = Given(N, HQ, D), Given(N, HKV, D), Given(N + 1, dtype=I32)
+OUT = dict(out=Q, lse=Given(N, HQ, dtype=F32))
+OUT_WS = dict(OUT, workspace=Given(1 << 20, dtype=U8))
+GRADS = dict(dq=Q, dk=KV, dv=KV, workspace=Given(1 << 20, dtype=U8))
+IDX, MASK = Given(N, dtype=I32), Given(N, N, dtype=U8)
+OLDER = {
+    "prefill": (lambda **kw: psa.prefill(Q, KV, KV, ROW, 0.1, **kw), OUT_WS),
+    "prefill_bwd": (lambda **kw: psa.prefill_bwd(Q, KV, KV, Q, ROW, Q, (ROW, ROW), 0.1, **kw), GRADS),
+    "verify": (lambda **kw: psa.verify(Q, KV, KV, KV, KV, ROW, 4, 0.1, 2, 1, **kw),
+               dict(OUT_WS, kv_indices=IDX)),
+    "verify_noalloc": (lambda **kw: psa.verify_noalloc(Q, KV, KV, KV, KV, ROW, 4, 0.1, 2, 1, **kw),
+                       OUT),
+    "verify_tree": (lambda **kw: psa.verify_tree(Q, KV, KV, KV, KV, ROW, 4, MASK, 0.1, 2, 1, **kw),
+                    dict(OUT_WS, kv_indices=IDX)),
+    "verify_extend": (lambda **kw: psa.verify_extend(Q, KV, KV, KV, KV, ROW, 4, ROW, 4, 0.1, nsplit=1,
+                                                     **kw),
+                      dict(OUT_WS, kv_indices=IDX, draft_mask=MASK, mask_indptr=ROW)),
+    "verify_fp8": (lambda **kw: psa.verify_fp8(Q, KV, KV, KV, KV, 1.0, 1.0, ROW, 4, 0.1, 2, 1, **kw),
+                   dict(OUT_WS, kv_indices=IDX)),
+    "verify_shared": (lambda **kw: psa.verify_shared(Q, KV, KV, KV, KV, 0.1, 2, 1, **kw),
+                      dict(OUT_WS, draft_mask=MASK)),
+    "sparse_latent": (lambda **kw: psa.sparse_latent(Q, Given(N, D), IDX2, 0.1, **kw), OUT),
+}
+IDX2 = Given(N, 2, dtype=I32)
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_attention_calls_check_given_buffers(name, library):
+    """Outputs, workspaces, tables, masks and status words on the host or
+    strided are refused, one at a time; as they should be, the call goes out."""
+    call, good = OLDER[name]
+    for key, t in good.items():
+        for bad in (Given(*t.shape, dtype=t.dtype, device="cpu"),
+                    Given(*t.shape, dtype=t.dtype, dense=False)):
+            with pytest.raises(ValueError):
+                call(**{**good, key: bad})
+    for bad in BAD_STATUS:
+        with pytest.raises(ValueError, match="status"):
+            call(**good, status=bad)
+    assert not library.calls
+    call(**good)
+    call(**good, status=Given(1, dtype=I32))
+    assert len(library.calls) == 2
