@@ -610,6 +610,8 @@ int psa_build_chunk_plan(const int32_t *qo_lens, const int32_t *kv_lens, int32_t
 size_t psa_chunk_workspace_size(const psa_chunk_info *info);
 
 /*
+ *   info       of the plan, as psa_build_chunk_plan gave it (fields that no
+ *              plan has: PSA_ERR_INVALID_ARG)
  *   q          device [T, Hq, d] bf16, T >= info->n_rows: the new tokens,
  *              request-major; rows behind n_rows are neither read nor written
  *   k_cache, v_cache  device [n_cache_tokens, Hkv, d], bf16 or (with

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "psa.h"
+#include "psa_chunk.h"
 #include "psa_internal.h"
 
 namespace psa {
@@ -758,13 +759,31 @@ extern "C" size_t psa_chunk_workspace_size(const psa_chunk_info* info) {
   return (o_bytes + 255) / 256 * 256 + (l_bytes + 255) / 256 * 256;
 }
 
+namespace {
+
+// Whether the fields are ones that the planner gives: they lead to divisions,
+// grids and buffer sizes.
+bool ok_info(const psa_chunk_info& i) {
+  if (i.Hq <= 0 || i.Hkv <= 0 || i.Hq % i.Hkv != 0 || i.window < 0 || i.n_ctas <= 0 ||
+      i.n_units <= 0 || i.n_joins < 0 || i.n_keys < i.n_rows ||
+      i.n_keys > INT32_MAX - 2 * kChunkTile || int64_t(i.n_rows) * i.Hq > INT32_MAX)
+    return false;
+  if (i.n_joins == 0 ? i.part_rows != 0 || i.max_join_rows != 0
+                     : i.part_rows <= 0 || i.part_rows > INT32_MAX || i.max_join_rows <= 0 ||
+                           i.max_join_rows > 256)
+    return false;
+  return i.len == ChunkPlanView(i.n_ctas, i.n_units, i.n_joins).len;
+}
+
+}  // namespace
+
 extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_cache,
                              int64_t n_cache_tokens, const int32_t* dev_kv_indices,
                              const psa_kv_scales* e4m3_scales, void* o, float* lse, int32_t T,
                              float scale, float logit_cap, const psa_chunk_info* info,
                              const int32_t* dev_plan, void* workspace, size_t ws_bytes,
                              int32_t* dev_status, void* stream) {
-  if (!info || T < info->n_rows || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
+  if (!info || info->n_rows < 0 || T < info->n_rows || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
       !(scale > 0.f) || !std::isfinite(scale) || !(logit_cap >= 0.f) ||
       !std::isfinite(logit_cap) || !ok_scales(e4m3_scales))
     return PSA_ERR_INVALID_ARG;
@@ -776,6 +795,9 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
       (logit_cap > 0.f && !std::isfinite(3.f * logit_scale / logit_cap)))
     return PSA_ERR_INVALID_ARG;
   if (info->n_rows == 0) return PSA_OK;
+  if (!ok_info(*info)) return PSA_ERR_INVALID_ARG;
+  if ((info->head_dim != 64 && info->head_dim != 128) || info->Hq / info->Hkv > 128)
+    return PSA_ERR_UNSUPPORTED;
   // without a page table the key positions are the cache's first rows
   if (!dev_kv_indices && info->n_keys > n_cache_tokens) return PSA_ERR_INVALID_ARG;
   if (!q || !k_cache || !v_cache || !o || !dev_plan || !aligned16(q) || !aligned16(k_cache) ||

@@ -333,3 +333,19 @@ def test_plan_takes_any_integers_and_windows_beyond_every_key():
     for window in (700, WIDE + 5, 2**70):
         data, info = psa.build_chunk_plan([3, 1], [700, 9], 8, 2, 128, window)
         assert (decode(data, info)[1] == whole).all() and info.window >= 700
+
+
+@pytest.mark.parametrize("fields", [
+    dict(Hq=0), dict(Hkv=0), dict(Hkv=-2), dict(Hq=9), dict(head_dim=0), dict(head_dim=96),
+    dict(head_dim=256), dict(Hq=258), dict(window=-1), dict(n_rows=-1), dict(n_keys=299),
+    dict(n_keys=2**31), dict(n_ctas=0), dict(n_units=0), dict(n_units=-1), dict(n_joins=-1),
+    dict(part_rows=-1), dict(part_rows=0), dict(part_rows=2**31), dict(max_join_rows=0),
+    dict(max_join_rows=257), dict(len=8), dict(Hq=2**31 - 2),
+])
+def test_call_refuses_an_info_that_no_plan_has(fields):
+    """The fields of a hand-made or stale info lead to divisions, grids and
+    buffer sizes: what cannot come from the planner is refused on the host."""
+    info = _info(**fields)
+    assert info.n_joins != 0  # split blocks: every field counts
+    rc = _chunk(info=info, T=300, ntok=3000, table=16)
+    assert rc in (psa.PSA_ERR_INVALID_ARG, psa.PSA_ERR_UNSUPPORTED)
