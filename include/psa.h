@@ -519,7 +519,9 @@ size_t psa_qk_norm_rope_bwd_workspace_size(int32_t head_dim);
  *                   (written; may be slices of one gradient tensor, or lie
  *                   exactly over dq_out or q, dk_out or k; PSA_ERR_INVALID_ARG
  *                   for any other overlap with an input or each other)
- *   dq_weight, dk_weight  device [d] fp32 (written, not added to; nullable)
+ *   dq_weight, dk_weight  device [d] fp32 (written, not added to; nullable).
+ *                   They and the workspace overlap nothing else here
+ *                   (PSA_ERR_INVALID_ARG)
  * The order of every sum depends on the sizes alone, so results repeat.
  * A token whose position is outside the table is left out, as above.
  */
@@ -623,18 +625,19 @@ size_t psa_chunk_workspace_size(const psa_chunk_info *info);
  *   logit_cap  0: none; c > 0: logits become c tanh(logit / c) before the mask
  *              (c <= 1000, PSA_ERR_UNSUPPORTED above: the cap is formed with an
  *              error of at most 1.5 * 2^-20 c)
- *   o          device [T, Hq, d] bf16 (written up to n_rows; PSA_ERR_INVALID_ARG if
- *              it overlaps q or a cache)
+ *   o          device [T, Hq, d] bf16 (written up to n_rows)
  *   lse        device [T, Hq] fp32 (written up to n_rows; nullable)
+ * o, lse and the workspace overlap neither one another nor q or a cache
+ * (PSA_ERR_INVALID_ARG).
  * Token i of request b is at position kv_lens[b] - qo_lens[b] + i and sees the
  * keys up to its own position, the last `window` of them if the plan has a
  * window.  The cache must hold the new tokens' keys already
  * (psa_cache_append).  With an e4m3 cache queries and weights are f16: |q|
  * must stay below 65504, elements of q below 2^-14 are off by up to 2^-25, and
- * weights below 2^-21 of their row's largest by up to 2^-32 of it.  A value (not a key) that is
- * not finite spoils every row of its 256-row block that shares its tile, as
- * in psa_prefill_fwd; rows of other requests and unused cache rows are never
- * touched.
+ * weights below 2^-21 of their row's largest by up to 2^-32 of it.  A value
+ * (not a key) that is not finite spoils every row of its 256-row block that
+ * shares its tile, as in psa_prefill_fwd; rows of other requests and unused
+ * cache rows are never touched.
  */
 int psa_chunk_fwd(const void *q, const void *k_cache, const void *v_cache,
                   int64_t n_cache_tokens, const int32_t *dev_kv_indices,

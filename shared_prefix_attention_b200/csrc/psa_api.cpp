@@ -557,6 +557,9 @@ bool apart(const RowsAt& out, const RowsAt& in, bool over) {
   return ahead >= out.width && ahead + in.width <= out.pitch;
 }
 
+// One run of bytes.
+RowsAt bytes_at(const void* at, size_t n) { return {at, int64_t(n), int64_t(n), 1}; }
+
 bool ok_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
 }  // namespace
@@ -646,6 +649,16 @@ extern "C" int psa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void*
         if (!apart(out[o], in[i], o == i) || !apart(out[o], up[i], o == i))
           return PSA_ERR_INVALID_ARG;
     if (!apart(out[0], out[1], false)) return PSA_ERR_INVALID_ARG;
+    const RowsAt sums[3] = {
+        bytes_at(workspace, psa_qk_norm_rope_bwd_workspace_size(head_dim)),
+        bytes_at(dq_weight, head_dim * sizeof(float)), bytes_at(dk_weight, head_dim * sizeof(float))};
+    for (int s = 0; s < 3; ++s) {
+      for (int i = 0; i < 2; ++i)
+        if (!apart(sums[s], in[i], false) || !apart(sums[s], up[i], false) ||
+            !apart(sums[s], out[i], false))
+          return PSA_ERR_INVALID_ARG;
+      if (!apart(sums[s], sums[(s + 1) % 3], false)) return PSA_ERR_INVALID_ARG;
+    }
   }
   RowsBwdArgs b = {};
   b.rows.q = q, b.rows.k = k;
@@ -806,17 +819,24 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
       (reinterpret_cast<uintptr_t>(dev_kv_indices) & 3u))
     return PSA_ERR_INVALID_ARG;
   // a block's rows are read while others are written already
-  const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), o_at = reinterpret_cast<uintptr_t>(o);
-  const uint64_t rows_bytes = uint64_t(T) * info->Hq * info->head_dim * 2;
-  if (q_at < o_at + rows_bytes && o_at < q_at + rows_bytes) return PSA_ERR_INVALID_ARG;
-  const int64_t row = int64_t(info->Hkv) * info->head_dim * (e4m3_scales ? 1 : 2);
-  for (const void* c : {k_cache, v_cache})
-    if (n_cache_tokens && !apart({o, int64_t(rows_bytes), int64_t(rows_bytes), 1},
-                                 {c, row, row, n_cache_tokens}, false))
-      return PSA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < psa_chunk_workspace_size(info) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const size_t rows = size_t(T) * info->Hq, ws_need = psa_chunk_workspace_size(info);
+  const size_t cache = size_t(n_cache_tokens) * info->Hkv * info->head_dim * (e4m3_scales ? 1 : 2);
+  const RowsAt in[3] = {bytes_at(q, rows * info->head_dim * 2),
+                        bytes_at(cache ? k_cache : nullptr, cache),
+                        bytes_at(cache ? v_cache : nullptr, cache)};
+  const RowsAt out[3] = {bytes_at(o, rows * info->head_dim * 2),
+                         bytes_at(lse, rows * sizeof(float)), bytes_at(workspace, ws_need)};
+  auto overlaps = [&](int k) {  // output k: an input or an output before it
+    for (const RowsAt& x : in)
+      if (!apart(out[k], x, false)) return true;
+    for (int j = 0; j < k; ++j)
+      if (!apart(out[k], out[j], false)) return true;
+    return false;
+  };
+  if (overlaps(0) || overlaps(1)) return PSA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < ws_need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PSA_ERR_WORKSPACE;
+  if (overlaps(2)) return PSA_ERR_INVALID_ARG;
   ChunkArgs a = {};
   a.q = q, a.kc = k_cache, a.vc = v_cache;
   a.n_cache = n_cache_tokens;

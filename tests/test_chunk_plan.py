@@ -335,6 +335,10 @@ def test_plan_takes_any_integers_and_windows_beyond_every_key():
         assert (decode(data, info)[1] == whole).all() and info.window >= 700
 
 
+MB = 1 << 20
+APART = dict(q=64 * MB, k=MB, v=8 * MB, o=128 * MB, lse=192 * MB, ws=256 * MB)
+
+
 @pytest.mark.parametrize("fields", [
     dict(Hq=0), dict(Hkv=0), dict(Hkv=-2), dict(Hq=9), dict(head_dim=0), dict(head_dim=96),
     dict(head_dim=256), dict(Hq=258), dict(window=-1), dict(n_rows=-1), dict(n_keys=299),
@@ -347,5 +351,5 @@ def test_call_refuses_an_info_that_no_plan_has(fields):
     buffer sizes: what cannot come from the planner is refused on the host."""
     info = _info(**fields)
     assert info.n_joins != 0  # split blocks: every field counts
-    rc = _chunk(info=info, T=300, ntok=3000, table=16)
+    rc = _chunk(info=info, T=300, ntok=3000, table=16, **APART)
     assert rc in (psa.PSA_ERR_INVALID_ARG, psa.PSA_ERR_UNSUPPORTED)

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import shared_prefix_attention_b200 as psa
-from test_chunk_plan import BAD_HOW, _append, _chunk, _how, _read
+from test_chunk_plan import BAD_HOW, _append, _chunk, _how, _info, _read
 from test_qk_norm_rope_gpu import EPS, angles, weight
 
 P = ctypes.c_void_p
@@ -74,6 +74,41 @@ def test_attention_refuses_an_output_over_a_cache():
     at = dict(q=64 * MB, k=MB, v=8 * MB)
     for o in (MB, 8 * MB + cache - 16, MB - rows + 16):
         assert _chunk(**at, o=o) == BAD, o
+
+
+def test_attention_refuses_overlaps_of_lse_and_workspace():
+    at = dict(q=64 * MB, k=MB, v=8 * MB, o=128 * MB, lse=192 * MB, ws=256 * MB)
+    rows, lse, cache = 300 * 8 * 128 * 2, 300 * 8 * 4, 2000 * 2 * 128 * 2
+    info = _info()
+    need = psa.lib().psa_chunk_workspace_size(ctypes.byref(info))
+    assert need > 256
+    for kw in (dict(lse=64 * MB), dict(lse=64 * MB + rows - 4), dict(lse=128 * MB), dict(lse=MB + 4),
+               dict(lse=128 * MB - lse + 4), dict(lse=8 * MB + cache - 4),
+               dict(ws=64 * MB), dict(ws=128 * MB + 256), dict(ws=MB), dict(ws=8 * MB),
+               dict(ws=192 * MB), dict(ws=128 * MB - (need - 256)), dict(lse=256 * MB + need - 4)):
+        assert _chunk(info=info, **{**at, **kw}) == BAD, kw
+
+
+def test_gradients_refuse_overlaps_of_weight_gradients_and_workspace():
+    at = dict(q=MB, k=2 * MB, gq=3 * MB, gk=4 * MB, dq=5 * MB, dk=6 * MB, dqw=7 * MB, dkw=8 * MB,
+              ws=9 * MB)
+    need = psa.lib().psa_qk_norm_rope_bwd_workspace_size(D)
+
+    def call(**kw):
+        a = {**at, **kw}
+        return psa.lib().psa_qk_norm_rope_bwd(
+            P(a["q"]), HQ * D, P(a["k"]), HKV * D, P(a["gq"]), P(a["gk"]), psa.PSA_BF16, T, HQ, HKV, D,
+            ctypes.byref(_how()), P(a["dq"]), HQ * D, P(a["dk"]), HKV * D, P(a["dqw"]), P(a["dkw"]),
+            P(a["ws"]), MB, None, None)
+
+    for w in ("dqw", "dkw"):
+        for x in ("q", "k", "gq", "gk", "dq", "dk", "ws"):
+            assert call(**{w: at[x]}) == BAD, (w, x)
+        assert call(**{w: 5 * MB + QB - 4}) == BAD
+    assert call(dkw=7 * MB + D * 4 - 4) == BAD  # on one another
+    for x in ("q", "k", "gq", "gk", "dq", "dk"):
+        assert call(ws=at[x]) == BAD, x
+        assert call(ws=at[x] - (need - 256)) == BAD, x
 
 
 @pytest.mark.gpu
