@@ -813,9 +813,14 @@ def cache_read(k_cache, v_cache, rows, k_scale: float | None = None,
 class ChunkPlan:
     """The work plan of :func:`chunk` for given lengths: the device copy of the
     lists, and what a call needs to know of them (``info``,
-    ``workspace_bytes``).  One plan serves any number of calls."""
+    ``workspace_bytes``).  One plan serves any number of calls, all layers of a
+    step among them.  Its sizes are part of a launch: a captured call replays
+    with its plan's lengths, other lengths need a plan and a capture of their
+    own."""
 
     def __init__(self, info: ChunkInfo, data: torch.Tensor, workspace_bytes: int):
+        if data.dtype is not _I32 or data.numel() < info.len or not data.is_contiguous():
+            raise ValueError(f"a chunk plan of {info.len} contiguous int32 words is needed")
         self.info, self.data, self.workspace_bytes = info, data, workspace_bytes
         # read once: a ctypes field costs a call's time
         self._ref = ctypes.byref(info)

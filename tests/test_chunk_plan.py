@@ -353,3 +353,15 @@ def test_call_refuses_an_info_that_no_plan_has(fields):
     assert info.n_joins != 0  # split blocks: every field counts
     rc = _chunk(info=info, T=300, ntok=3000, table=16, **APART)
     assert rc in (psa.PSA_ERR_INVALID_ARG, psa.PSA_ERR_UNSUPPORTED)
+
+
+def test_plan_object_checks_its_lists():
+    """Lists that are shorter than the plan's length, or not int32 words, are
+    not what a kernel may read."""
+    data, info = psa.build_chunk_plan([4], [4], 2, 2, 128)
+    whole = torch.from_numpy(data)
+    for bad in (whole[:-1], whole.long(), whole.float(), torch.stack([whole, whole], 1)[:, 0]):
+        with pytest.raises(ValueError, match="plan"):
+            psa.ChunkPlan(info, bad, 256)
+    psa.ChunkPlan(info, whole, 256)
+    psa.ChunkPlan(info, torch.cat([whole, whole]), 256)
