@@ -38,11 +38,13 @@
 //                the log2 domain with lazy rescaling, and the epilogue: final
 //                rows, or a partial (O / l and log2-sum-exp, fp32) for the
 //                join kernel.
-// What bounds it (one long prompt's piece, 2048 tokens over 16k keys, 480 us =
-// 1.2 PFLOP/s, SM clock 1.66 GHz under the power limit): the special-function
-// unit and the tensor pipe are each busy 60 % of the time; a tile's chain QK,
-// softmax, PV (about 3400 cycles) is longer than either's share of it (2050),
-// and two halves are all that TMEM holds.
+// What bounds it (one long prompt's piece, 2048 tokens over 16k keys: 470 us =
+// 1.24 PFLOP/s in runs of a few ms; 546 us = 1.07 PFLOP/s in long ones, whose
+// SM clock the power limit holds at 1.66 GHz): the special-function unit and
+// the tensor pipe are each busy 60 % of the time; a tile's chain QK, softmax,
+// PV (about 3400 cycles) is longer than either's share of it (2050), and two
+// halves are all that TMEM holds.  Over a page table the gather of a tile takes
+// nearly as long as that chain.
 // P is rounded to bf16 (f16 over an e4m3 cache) for the tensor cores: at most
 // half a step per weight, averaged over the keys; the sum l keeps fp32.  f16
 // steps stop shrinking at 2^-14, so those weights are held 2^7 up (kLift): one
@@ -321,9 +323,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // step of fp32, 1 / (1 + e) is off by 7 U of itself (sum, two products, 2 U of
 // the reciprocal, two products) and 2 U (a quarter of the exponential's and its
 // argument's), which counts twice c'; c', the offset, the last sum: 24 U c' in
-// all (test: logits to 4.5 c at c = 1000).  A further
-// step, a part of the first exponentials by a polynomial on the FMA pipe,
-// gained 2 %: the issue slots are then as full as the unit.
+// all (test: logits to 4.5 c at c = 1000).  (A part of the first exponentials
+// by a polynomial on the FMA pipe changed the time by 2 %; not kept.)
 template <bool F16, bool MASKED, int N>
 __device__ __forceinline__ float weights_row_capped(uint32_t (&s)[N], float neg_m,
                                                     const Params& p) {
@@ -1138,7 +1139,8 @@ int launch_chunk_of(const ChunkArgs& a) {
   // few rows through a page table, where gathering sets the pace (18 requests'
   // single tokens over 16k keys: 243 us against 211; contiguous, by TMA, 186
   // against 188).  For full blocks over bf16 its softmax costs more than its
-  // loaders gain: 410 us against 425 on 16k paged histories.
+  // loaders gain: 410 us against 425 on 16k paged histories.  The form is the
+  // whole batch's: single tokens beside a prompt's piece go through the narrow one.
   if (a.e4m3) return launch_chunk_cap<D, true, true>(a);
   return a.info.all_twin && a.kv_indices ? launch_chunk_cap<D, false, true>(a)
                                          : launch_chunk_cap<D, false, false>(a);

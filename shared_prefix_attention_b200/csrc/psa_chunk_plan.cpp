@@ -22,7 +22,7 @@ constexpr int kTile = psa::kChunkTile;
 // tiles of the same rows, so a tile costs less: the loaders set its pace, and
 // 64-wide heads give them half the bytes (3 x 777 tokens of 16 such heads,
 // capped: 132 us at 0.7 against 138 at 0.8; uncapped 74.5 / 76.8, and 79.8 at
-// 0.6).  A piece pays for its first tile's latency and its epilogue, a split
+// 0.6; e4m3 82.3 / 85.4; with four query heads to a KV head 135.5 / 133.9).  A piece pays for its first tile's latency and its epilogue, a split
 // block for its partial rows and the join launch.
 constexpr double kTwinTile = 0.8, kTwinTile64 = 0.7;
 constexpr double kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
@@ -211,6 +211,8 @@ int build(const int32_t* qo_lens, const int32_t* kv_lens, int32_t B, int32_t Hq,
     // of a head at any time: where the keys and values do not fit L2 they come
     // from memory more than once.  Measured, pieces against filled lists: 586
     // and 556 us with 75 MB of keys and values, 454 and 482 us with 290 MB.
+    // (Counted as bf16 and whole: an e4m3 cache or a window may fit L2 where
+    // this says that it does not; the plan is not told the cache's type.)
     const double kv_bytes = 4.0 * double(kv0) * Hkv * head_dim;
     if (found) offer(std::move(fill), kv_bytes > 120e6 ? 1.08 : 1.0);
   }
