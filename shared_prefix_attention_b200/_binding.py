@@ -833,9 +833,13 @@ _INT32_MAX = 2**31 - 1
 def _int32s(x, name: str):
     """x as int32 values, none of them changed on the way."""
     given = np.asarray(x)
-    with np.errstate(invalid="ignore"):
-        out = given.astype(np.int32)
-    if not (out == given).all():
+    try:
+        with np.errstate(invalid="ignore"):
+            out = given.astype(np.int32)
+        same = (out == given).all()
+    except OverflowError:
+        same = False
+    if not same:
         raise ValueError(f"{name}: whole numbers of 32 bits are needed")
     return out
 

@@ -305,6 +305,7 @@ WIDE = 2**32
     (torch.tensor([1]), torch.tensor([WIDE + 100]), 8, 2, 128),
     (np.array([1], dtype=np.uint64), np.array([2**64 - 1], dtype=np.uint64), 8, 2, 128),
     ([1], [WIDE + 100], 8, 2, 128),
+    ([1], [2**70], 8, 2, 128),
     ([1], [100.5], 8, 2, 128),
     ([0.5], [100], 8, 2, 128),
     ([1], [float("nan")], 8, 2, 128),
