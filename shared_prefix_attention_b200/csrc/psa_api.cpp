@@ -796,7 +796,8 @@ extern "C" int psa_chunk_fwd(const void* q, const void* k_cache, const void* v_c
                              float scale, float logit_cap, const psa_chunk_info* info,
                              const int32_t* dev_plan, void* workspace, size_t ws_bytes,
                              int32_t* dev_status, void* stream) {
-  if (!info || info->n_rows < 0 || T < info->n_rows || n_cache_tokens < 0 || n_cache_tokens > INT32_MAX ||
+  if (!info || info->n_rows < 0 || T < info->n_rows || n_cache_tokens < 0 ||
+      n_cache_tokens > INT32_MAX ||
       !(scale > 0.f) || !std::isfinite(scale) || !(logit_cap >= 0.f) ||
       !std::isfinite(logit_cap) || !ok_scales(e4m3_scales))
     return PSA_ERR_INVALID_ARG;

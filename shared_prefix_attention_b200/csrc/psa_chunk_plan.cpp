@@ -22,8 +22,9 @@ constexpr int kTile = psa::kChunkTile;
 // tiles of the same rows, so a tile costs less: the loaders set its pace, and
 // 64-wide heads give them half the bytes (3 x 777 tokens of 16 such heads,
 // capped: 132 us at 0.7 against 138 at 0.8; uncapped 74.5 / 76.8, and 79.8 at
-// 0.6; e4m3 82.3 / 85.4; with four query heads to a KV head 135.5 / 133.9).  A piece pays for its first tile's latency and its epilogue, a split
-// block for its partial rows and the join launch.
+// 0.6; e4m3 82.3 / 85.4; with four query heads to a KV head 135.5 / 133.9).
+// A piece pays for its first tile's latency and its epilogue, a split block
+// for its partial rows and the join launch.
 constexpr double kTwinTile = 0.8, kTwinTile64 = 0.7;
 constexpr double kPieceCost = 1.2, kSplitCost = 0.4, kJoinCost = 1.5;
 
